@@ -81,6 +81,15 @@ _SIGS = {
     "coda_mx_quantize": (_ST, [_P, _I64, _I64, ctypes.c_int, _P, _P, _P]),
     "coda_gemm_res_partialrms_mx": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
     "coda_gemm_rowscale_partial_mx": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _F, _P, _P, _I64, _I64, _I64, _P]),
+    "coda_embed": (_ST, [_P, _P, _F, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "coda_embed_bwd_workspace_size": (_SZ, [_I64, _I64]),
+    "coda_embed_bwd": (_ST, [_P, _P, _F, _P, ctypes.c_int, _P, _SZ, _I64, _I64, _I64, _P]),
+    "coda_add_rmsnorm_mx": (_ST, [_P, _P, _P, _F, _P, _P, _P, _P, _I64, _I64, _P]),
+    "coda_add_rmsnorm_fp8": (_ST, [_P, _P, _P, _F, _P, _P, _P, _P, _P, _I64, _I64, _P]),
+    "coda_add_rmsnorm_bwd_workspace_size": (_SZ, [_I64, _I64]),
+    "coda_add_rmsnorm_bwd": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _SZ, _I64, _I64, _P]),
+    "coda_newton_schulz_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "coda_newton_schulz": (_ST, [_P, _P, _I64, _I64, _I64, ctypes.c_int, _F, _F, _F, _F, _P, _SZ, _P]),
 }
 
 _lib = None
@@ -799,3 +808,155 @@ def block_backward(dOut, x, W1, W2, gamma, fwd):
     dh, dgamma = rms_reduce_bwd(pdr, fwd["r"], d_hg, fwd["h"], gamma)
     dx, dW1 = gemm_res_partialrms_bwd(dh, x, W1)
     return {"dW2": dW2, "dgamma": dgamma, "dh": dh, "dres": dh, "dx": dx, "dW1": dW1, "d_hg": d_hg, "pdr": pdr}
+
+
+# ------------------------------------------------ around the GEMM chain
+#
+# These calls run on the device of their tensors (which must all be on one),
+# on that device's current stream.
+
+
+def _on_one_device(**tensors):
+    """A guard for the device that all of the given tensors are on."""
+    devs = {t.device for t in tensors.values() if t is not None}
+    if len(devs) != 1:
+        raise ValueError("tensors on different devices: " + ", ".join(
+            f"{k} on {t.device}" for k, t in tensors.items() if t is not None))
+    return torch.cuda.device(devs.pop())
+
+
+def _workspace(ws, nbytes: int, like):
+    """The caller's workspace (a byte tensor; the library checks its size), or a new one."""
+    if ws is None:
+        return _empty((max(nbytes, 16),), U8, like)
+    return _need(ws, U8, "ws")
+
+
+def _matrix(t, dtype, name):
+    _need(t, dtype, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
+    return tuple(t.shape)
+
+
+def embed(tokens, E, scale: float = 1.0, gamma=None, *, h=True, partial=True, h_out=None, hg_out=None,
+          partial_out=None):
+    """h = scale * E[tokens]; with gamma also hg = gamma * h; partial[t, i] =
+    sum of h_ij^2 over column slot t: the inputs of gemm_rowscale_partial and,
+    after rms_reduce, of gemm_swiglu.  tokens [M] int64; one outside [0, V)
+    gives a zero row.  Returns (h, hg, partial); entries not requested are None."""
+    V, D = _matrix(E, BF16, "E")
+    _need(tokens, torch.int64, "tokens")
+    M = tokens.numel()
+    _need(tokens, torch.int64, "tokens", (M,))
+    if gamma is not None:
+        _need(gamma, BF16, "gamma", (D,))
+    elif hg_out is not None:
+        raise ValueError("hg_out needs gamma")
+    h_out = (_empty((M, D), BF16, E) if h_out is None else _need(h_out, BF16, "h_out", (M, D))) if h else None
+    if gamma is not None:
+        hg_out = _empty((M, D), BF16, E) if hg_out is None else _need(hg_out, BF16, "hg_out", (M, D))
+    T = partial_cols(D)
+    if partial:
+        partial_out = _empty((T, M), F32, E) if partial_out is None else _need(partial_out, F32, "partial_out", (T, M))
+    else:
+        partial_out = None
+    with _on_one_device(tokens=tokens, E=E, gamma=gamma, h_out=h_out, hg_out=hg_out, partial_out=partial_out):
+        _call("coda_embed", _ptr(tokens), _ptr(E), float(scale), _ptr(gamma), _ptr(h_out), _ptr(hg_out),
+              _ptr(partial_out), M, D, V, _stream())
+    return h_out, hg_out, partial_out
+
+
+def embed_bwd(tokens, dh, V: int, scale: float = 1.0, dE_out=None, accumulate: bool = False, ws=None):
+    """dE[v] = scale * sum of dh_i over the rows i with token v, [V, D] fp32
+    (repeatable bits).  accumulate adds to dE_out and touches only the rows of
+    tokens that occur."""
+    M, D = _matrix(dh, BF16, "dh")
+    _need(tokens, torch.int64, "tokens", (M,))
+    if accumulate and dE_out is None:
+        raise ValueError("accumulate needs dE_out")
+    dE_out = _empty((int(V), D), F32, dh) if dE_out is None else _need(dE_out, F32, "dE_out", (int(V), D))
+    ws = _workspace(ws, int(load_library().coda_embed_bwd_workspace_size(M, D)), dh)
+    with _on_one_device(tokens=tokens, dh=dh, dE_out=dE_out, ws=ws):
+        _call("coda_embed_bwd", _ptr(tokens), _ptr(dh), float(scale), _ptr(dE_out), 1 if accumulate else 0, _ptr(ws),
+              ws.numel(), M, D, int(V), _stream())
+    return dE_out
+
+
+def _norm_inputs(x, res, gamma, h, h_out, r_out):
+    M, N = _matrix(x, BF16, "x")
+    if res is not None:
+        _need(res, BF16, "res", (M, N))
+    _need(gamma, BF16, "gamma", (N,))
+    h_out = (_empty((M, N), BF16, x) if h_out is None else _need(h_out, BF16, "h_out", (M, N))) if h else None
+    r_out = _empty((M,), F32, x) if r_out is None else _need(r_out, F32, "r_out", (M,))
+    return M, N, h_out, r_out
+
+
+def add_rmsnorm_mx(x, res, gamma, eps: float, *, h=True, h_out=None, yq_out=None, ysf_out=None, r_out=None):
+    """h = x + res (res may be None), y = gamma * h / sqrt(mean(h^2) + eps) in
+    MXFP8 for gemm_rowscale_partial_mx.  Returns (h bf16 or None, codes uint8
+    [M, N], scales uint8 in the A layout, r [M])."""
+    M, N, h_out, r_out = _norm_inputs(x, res, gamma, h, h_out, r_out)
+    yq_out = _empty((M, N), U8, x) if yq_out is None else _need(yq_out, U8, "yq_out", (M, N))
+    nsf = mx_sf_bytes(M, N, MX_A) if M else 0
+    ysf_out = _empty((nsf,), U8, x) if ysf_out is None else _need(ysf_out, U8, "ysf_out", (nsf,))
+    with _on_one_device(x=x, res=res, gamma=gamma, h_out=h_out, yq_out=yq_out, ysf_out=ysf_out, r_out=r_out):
+        _call("coda_add_rmsnorm_mx", _ptr(x), _ptr(res), _ptr(gamma), float(eps), _ptr(h_out), _ptr(yq_out),
+              _ptr(ysf_out), _ptr(r_out), M, N, _stream())
+    return h_out, yq_out, ysf_out, r_out
+
+
+def add_rmsnorm_fp8(x, res, gamma, eps: float, s_y, *, h=True, h_out=None, y8_out=None, amax_out=None, r_out=None):
+    """h = x + res (res may be None), y8 = e4m3(gamma * h * r / s_y) for
+    gemm_fp8, amax = max |y|.  Returns (h bf16 or None, y8 uint8 [M, N], amax
+    [1], r [M])."""
+    M, N, h_out, r_out = _norm_inputs(x, res, gamma, h, h_out, r_out)
+    _need(s_y, F32, "s_y", (1,))
+    y8_out = _empty((M, N), U8, x) if y8_out is None else _need(y8_out, U8, "y8_out", (M, N))
+    amax_out = _empty((1,), F32, x) if amax_out is None else _need(amax_out, F32, "amax_out", (1,))
+    with _on_one_device(x=x, res=res, gamma=gamma, s_y=s_y, h_out=h_out, y8_out=y8_out, amax_out=amax_out,
+                        r_out=r_out):
+        _call("coda_add_rmsnorm_fp8", _ptr(x), _ptr(res), _ptr(gamma), float(eps), _ptr(s_y), _ptr(h_out),
+              _ptr(y8_out), _ptr(amax_out), _ptr(r_out), M, N, _stream())
+    return h_out, y8_out, amax_out, r_out
+
+
+def add_rmsnorm_bwd(dy, h, r, gamma, d_h=None, dx_out=None, dgamma_out=None, ws=None):
+    """Backward of add_rmsnorm_mx / add_rmsnorm_fp8 from the saved h and r: dx
+    (of x and of res; d_h, the residual stream's gradient, is added) bf16 and
+    dgamma fp32.  Returns (dx, dgamma)."""
+    M, N = _matrix(dy, BF16, "dy")
+    _need(h, BF16, "h", (M, N))
+    _need(r, F32, "r", (M,))
+    _need(gamma, BF16, "gamma", (N,))
+    if d_h is not None:
+        _need(d_h, BF16, "d_h", (M, N))
+    dx_out = _empty((M, N), BF16, dy) if dx_out is None else _need(dx_out, BF16, "dx_out", (M, N))
+    dgamma_out = _empty((N,), F32, dy) if dgamma_out is None else _need(dgamma_out, F32, "dgamma_out", (N,))
+    ws = _workspace(ws, int(load_library().coda_add_rmsnorm_bwd_workspace_size(M, N)), dy)
+    with _on_one_device(dy=dy, h=h, r=r, gamma=gamma, d_h=d_h, dx_out=dx_out, dgamma_out=dgamma_out, ws=ws):
+        _call("coda_add_rmsnorm_bwd", _ptr(dy), _ptr(h), _ptr(r), _ptr(gamma), _ptr(d_h), _ptr(dx_out),
+              _ptr(dgamma_out), _ptr(ws), ws.numel(), M, N, _stream())
+    return dx_out, dgamma_out
+
+
+NEWTON_SCHULZ_COEFFS = (3.4445, -4.775, 2.0315)  # the Muon optimiser's
+
+
+def newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: float = 1e-7, out=None, ws=None):
+    """Orthogonalised update of a weight from its fp32 gradient or momentum G
+    [m, n] (or several, [batch, m, n]): X = G / (|G| + eps), then `steps` times
+    X <- a X + (b A + c A^2) X with A = X X^T.  Returns bf16 of G's shape."""
+    _need(G, F32, "G")
+    if G.dim() not in (2, 3):
+        raise ValueError(f"G must be [m, n] or [batch, m, n], got shape {tuple(G.shape)}")
+    a, b, c = (float(v) for v in coeffs)
+    batch = G.shape[0] if G.dim() == 3 else 1
+    m, n = G.shape[-2:]
+    out = _empty(tuple(G.shape), BF16, G) if out is None else _need(out, BF16, "out", tuple(G.shape))
+    ws = _workspace(ws, int(load_library().coda_newton_schulz_workspace_size(batch, m, n)), G)
+    with _on_one_device(G=G, out=out, ws=ws):
+        _call("coda_newton_schulz", _ptr(G), _ptr(out), batch, m, n, int(steps), a, b, c, float(eps), _ptr(ws),
+              ws.numel(), _stream())
+    return out

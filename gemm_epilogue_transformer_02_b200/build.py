@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcoda.so")
 
 SOURCES = ["coda.cu"]
-DEPS = ["coda.cu", "coda_device.cuh", "coda_gemm.cuh", "coda_rowops.cuh", "coda_block.cuh", "coda_grouped.cuh"]
+DEPS = ["coda.cu", "coda_device.cuh", "coda_gemm.cuh", "coda_rowops.cuh", "coda_block.cuh", "coda_grouped.cuh",
+        "train/coda_train_api.cuh", "train/coda_embed.cuh", "train/coda_norm8.cuh", "train/coda_ns.cuh"]
 
 
 def nvcc_path() -> str:

@@ -19,7 +19,7 @@ namespace {
 using namespace coda;
 
 constexpr int64_t kPartialTile = 128;  // columns per partial sum: one half of a 256-column tile
-constexpr int kVersion = 3;  // 2: partial sums per 128-column slot; 3: the MXFP8 calls
+constexpr int kVersion = 4;  // 2: partial sums per 128-column slot; 3: the MXFP8 calls; 4: embedding, 8-bit norms, Newton-Schulz
 
 int64_t g_wait_ns = 1000000000LL;
 
@@ -1795,3 +1795,5 @@ extern "C" coda_status_t coda_rms_reduce_bwd_noalloc(const float* pdr, const flo
                                                                         static_cast<int>(N), dgamma_out);
   return cudaGetLastError() == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
 }
+
+#include "train/coda_train_api.cuh"

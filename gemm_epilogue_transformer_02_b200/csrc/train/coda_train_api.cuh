@@ -1,0 +1,455 @@
+// Host side of the training-step calls around the GEMM chain: token embedding,
+// residual add + RMSNorm with 8-bit outputs, Newton-Schulz orthogonalisation.
+// Included by coda.cu (it uses its validation, device and tensor-map helpers);
+// contracts in include/coda.h.
+#pragma once
+
+#include "coda_embed.cuh"
+#include "coda_norm8.cuh"
+#include "coda_ns.cuh"
+
+namespace {
+
+constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
+
+// A launch with programmatic stream serialisation (the kernel waits for the
+// previous one itself), as the GEMMs'.  cluster 0: none.
+template <class... KArgs, class... Args>
+coda_status_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                         Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, KArgs(args)...) == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
+}
+
+// Sets a kernel's dynamic shared memory limit once per device.
+template <class K>
+coda_status_t set_smem(K kern, int bytes, int dev, bool (&done)[64]) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (done[dev]) return CODA_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return CODA_ERR_LAUNCH;
+  done[dev] = true;
+  return CODA_OK;
+}
+
+// ---------------------------------------------------------------- embedding
+
+// Pairs per block of the embedding backward: 32, so that a batch of some
+// thousand tokens gives a few hundred blocks; more once that would make over
+// 2048 blocks, which bounds the parts a run over many chunks is joined from.
+inline int embed_chunk(int64_t M) {
+  int64_t c = 32;
+  while (c < coda::kEmbBwdMaxChunk && M > 2048 * c) c *= 2;
+  return static_cast<int>(c);
+}
+
+struct EmbedWs {
+  size_t buf0, buf1, part, bytes;
+  int chunk, items;
+};
+
+inline EmbedWs embed_ws(int64_t M, int64_t D) {
+  EmbedWs w;
+  w.chunk = embed_chunk(M);
+  w.items = static_cast<int>((M + w.chunk - 1) / w.chunk);
+  w.buf0 = 0;
+  w.buf1 = align256(static_cast<size_t>(M) * 8);
+  w.part = 2 * w.buf1;
+  w.bytes = w.part + align256(static_cast<size_t>(w.items) * 2 * D * 4);
+  return w;
+}
+
+// --------------------------------------------------------------------- norm
+
+// A row's block: two 8-column vectors a thread (one for rows of up to 512), so
+// a row of up to 16384 columns stays in one block's registers.
+constexpr int64_t kNorm8MaxN = 16384;
+inline int norm8_vpt(int64_t N) { return N <= 512 ? 1 : 2; }
+inline int norm8_threads(int64_t N) {
+  const int64_t t = (N / 8 + norm8_vpt(N) - 1) / norm8_vpt(N);
+  return static_cast<int>((t + 31) & ~int64_t(31));
+}
+
+template <bool MX>
+coda_status_t launch_norm8(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float eps, const float* s_y,
+                           uint16_t* h_out, uint8_t* q, uint8_t* sf, unsigned* amax, float* r_out, int64_t M,
+                           int64_t N, cudaStream_t s) {
+  const int64_t nrb = (M + 127) / 128;
+  auto kern = norm8_vpt(N) == 1 ? add_rmsnorm_kernel<MX, 1> : add_rmsnorm_kernel<MX, 2>;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(MX ? nrb * 128 : M)), norm8_threads(N), 0, 0, s,
+                    reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(res),
+                    reinterpret_cast<const __nv_bfloat16*>(gamma), eps, s_y, reinterpret_cast<__nv_bfloat16*>(h_out),
+                    q, sf, amax, r_out, M, static_cast<int>(N), static_cast<int>(nrb));
+}
+
+// Blocks of the norm's backward: 768 threads' worth for each of 148 SMs.
+inline int norm8_bwd_blocks(int64_t M, int64_t N) {
+  const int64_t b = std::max<int64_t>(1, 148 * 768 / norm8_threads(N));
+  return static_cast<int>(std::min<int64_t>(M, b));
+}
+
+// ------------------------------------------------------------ Newton-Schulz
+
+constexpr int kNsMaxNormBlocks = 512;
+
+struct NsPlan {
+  int64_t batch, m, n, s;  // s: the smaller side
+  bool tall;
+  int block;     // tile of the symmetric results: 256 (CTA pairs) or 128
+  bool pair_up;  // the update runs on CTA pairs
+  int norm_blocks;
+  size_t hi[2], lo[2], A, B, dA, dB, part, bytes;
+};
+
+inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
+  NsPlan p;
+  p.batch = batch;
+  p.m = m;
+  p.n = n;
+  p.tall = m > n;
+  p.s = p.tall ? n : m;
+  p.block = p.s >= 1024 ? 256 : 128;
+  p.pair_up = p.block == 256;
+  const int64_t n8 = m * n / 8;
+  p.norm_blocks = static_cast<int>(std::min<int64_t>(kNsMaxNormBlocks, (n8 + 2047) / 2048));
+  size_t o = 0;
+  const size_t x = align256(static_cast<size_t>(batch) * m * n * 2);
+  const size_t sq = align256(static_cast<size_t>(batch) * p.s * p.s * 2);
+  const size_t dg = align256(static_cast<size_t>(batch) * p.s * 4);
+  for (int i = 0; i < 2; ++i) {
+    p.hi[i] = o;
+    p.lo[i] = o + x;
+    o += 2 * x;
+  }
+  p.A = o;
+  p.B = o + sq;
+  p.dA = o + 2 * sq;
+  p.dB = p.dA + dg;
+  p.part = p.dB + dg;
+  p.bytes = p.part + align256(static_cast<size_t>(batch) * p.norm_blocks * 8);
+  return p;
+}
+
+// [batch, rows, cols] of 2-byte elements, box box_rows x 64, 128-byte swizzle;
+// out-of-range elements read as zero and are not written.
+bool tmap3d(CUtensorMap* m, const void* base, bool bf16, uint64_t cols, uint64_t rows, uint64_t batch,
+            uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {cols, rows, batch};
+  cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// An operand with `rows` output rows (or columns) and K: stored [rows, K], [K, rows] or symmetric.
+bool ns_operand(NsOperand* o, const void* p, int major, uint64_t rows, uint64_t K, uint64_t batch) {
+  o->major = major;
+  bool ok = true;
+  if (major != kNsMN) ok = ok && tmap3d(&o->k, p, false, K, rows, batch, 128);
+  if (major != kNsK) ok = ok && tmap3d(&o->mn, p, false, rows, K, batch, 64);
+  return ok;
+}
+
+template <int KIND, bool PAIR>
+coda_status_t ns_launch(int dev, DevInfo* info, NsParams& p, cudaStream_t stream) {
+  static bool done[64];
+  static int clusters[64];
+  auto kern = ns_gemm_kernel<KIND, PAIR>;
+  constexpr int kTile = PAIR ? 256 : 128;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!done[dev]) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmemBytes) != cudaSuccess)
+        return CODA_ERR_LAUNCH;
+      clusters[dev] = info->sms;
+      if (PAIR) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(2 * (info->sms / 2), 1, 1);
+        cfg.blockDim = dim3(kNsThreads, 1, 1);
+        cfg.dynamicSmemBytes = kNsSmemBytes;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+          cudaGetLastError();
+          n = info->sms / 2;
+        }
+        clusters[dev] = n;
+      }
+      done[dev] = true;
+    }
+  }
+  p.n_rt = (p.rows + kTile - 1) / kTile;
+  p.n_ct = (p.cols + kTile - 1) / kTile;
+  const int64_t tiles = KIND == kNsUpdate ? static_cast<int64_t>(p.n_rt) * p.n_ct
+                                          : static_cast<int64_t>(p.n_rt) * (p.n_rt + 1) / 2;
+  if (tiles * p.batch > kMaxInt) return CODA_ERR_SHAPE;
+  p.tiles = static_cast<int>(tiles);
+  p.wait_ns = static_cast<uint64_t>(g_wait_ns);
+  const int units = p.tiles * p.batch;
+  const int n = units < clusters[dev] ? units : clusters[dev];
+  return launch_pdl(kern, dim3(static_cast<unsigned>(PAIR ? 2 * n : n)), kNsThreads, kNsSmemBytes, PAIR ? 2 : 0,
+                    stream, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+coda_status_t coda_embed(const int64_t* tokens, const uint16_t* E, float scale, const uint16_t* gamma, uint16_t* h_out,
+                         uint16_t* hg_out, float* partial, int64_t M, int64_t D, int64_t V, void* stream) {
+  CODA_CHECK(M >= 0 && M <= kMaxInt && dim_ok(D) && V > 0 && V < kMaxInt, CODA_ERR_SHAPE);
+  CODA_CHECK(tokens && E && (h_out || hg_out || partial) && (!hg_out || gamma), CODA_ERR_NULL);
+  CODA_CHECK(al16(tokens) && al16(E) && al16(gamma) && al16(h_out) && al16(hg_out) && al16(partial), CODA_ERR_ALIGN);
+  if (M == 0) return CODA_OK;
+  int dev;
+  DevInfo* info;
+  const coda_status_t st = current_device(&dev, &info);
+  if (st != CODA_OK) return st;
+  const int64_t nspan = (D + 255) / 256;
+  const int64_t items = (M + kEmbRows - 1) / kEmbRows * nspan;
+  const int64_t blocks = (items + kEmbWarps - 1) / kEmbWarps;
+  CODA_CHECK(blocks <= kMaxInt, CODA_ERR_SHAPE);
+  return launch_pdl(embed_kernel, dim3(static_cast<unsigned>(blocks)), 32 * kEmbWarps, 0, 0,
+                    static_cast<cudaStream_t>(stream), tokens, reinterpret_cast<const __nv_bfloat16*>(E), scale,
+                    reinterpret_cast<const __nv_bfloat16*>(gamma), reinterpret_cast<__nv_bfloat16*>(h_out),
+                    reinterpret_cast<__nv_bfloat16*>(hg_out), partial, M, static_cast<int>(D), V,
+                    static_cast<int>(nspan));
+}
+
+size_t coda_embed_bwd_workspace_size(int64_t M, int64_t D) {
+  if (M <= 0 || M > kMaxInt || !dim_ok(D)) return 0;
+  return embed_ws(M, D).bytes;
+}
+
+coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float scale, float* dE, int accumulate, void* ws,
+                             size_t ws_bytes, int64_t M, int64_t D, int64_t V, void* stream) {
+  CODA_CHECK(M >= 0 && M <= kMaxInt && dim_ok(D) && V > 0 && V < kMaxInt, CODA_ERR_SHAPE);
+  CODA_CHECK(dE && (M == 0 || (tokens && dh)), CODA_ERR_NULL);
+  CODA_CHECK(al16(tokens) && al16(dh) && al16(dE) && al16(ws), CODA_ERR_ALIGN);
+  CODA_CHECK(M == 0 || (ws && ws_bytes >= embed_ws(M, D).bytes), CODA_ERR_WORKSPACE);
+  if (M == 0 && accumulate) return CODA_OK;
+  int dev;
+  DevInfo* info;
+  coda_status_t st = current_device(&dev, &info);
+  if (st != CODA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0)
+    return cudaMemsetAsync(dE, 0, static_cast<size_t>(V) * D * 4, s) == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
+  static bool done[64];
+  st = set_smem(embed_sort_kernel, kSortSmem, dev, done);
+  if (st != CODA_OK) return st;
+  const EmbedWs w = embed_ws(M, D);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int2* b0 = reinterpret_cast<int2*>(base + w.buf0);
+  int2* b1 = reinterpret_cast<int2*>(base + w.buf1);
+  float* part = reinterpret_cast<float*>(base + w.part);
+  int bits = 1;
+  while ((V >> bits) > 0) ++bits;  // keys 0 .. V
+  const int passes = (bits + kSortBits - 1) / kSortBits;
+  // pass 0 reads the tokens and writes b1, pass 1 writes b0, ...
+  const int2* pairs = passes & 1 ? b1 : b0;
+  const size_t n16 = accumulate ? 0 : static_cast<size_t>(V) * D / 4;
+  // zeroing: enough clusters that each thread stores 64 bytes or more, at most
+  // one 1024-thread CTA per SM beside the sorting ones
+  const int64_t zc = std::min<int64_t>(info->sms / kSortCluster,
+                                       static_cast<int64_t>((n16 + 4 * kSortThreads * kSortCluster - 1) /
+                                                            (4 * kSortThreads * kSortCluster)));
+  st = launch_pdl(embed_sort_kernel, dim3(static_cast<unsigned>(kSortCluster * (1 + zc))), kSortThreads, kSortSmem, 0,
+                  s, tokens, static_cast<int>(M), V, passes, b0, b1, reinterpret_cast<uint4*>(dE), n16);
+  if (st != CODA_OK) return st;
+  const int threads = static_cast<int>(std::min<int64_t>(kEmbBwdThreads, (D / 8 + 31) & ~int64_t(31)));
+  st = launch_pdl(embed_bwd_kernel,
+                  dim3(static_cast<unsigned>(w.items), static_cast<unsigned>((D + 8 * kEmbBwdThreads - 1) / (8 * kEmbBwdThreads))),
+                  threads, 0, 0, s, pairs, reinterpret_cast<const __nv_bfloat16*>(dh), scale, dE, part,
+                  static_cast<int>(M), V, static_cast<int>(D), w.chunk, accumulate ? 1 : 0);
+  if (st != CODA_OK || w.items == 1) return st;
+  return launch_pdl(embed_bwd_join_kernel, dim3(static_cast<unsigned>(w.items - 1), static_cast<unsigned>((D + 255) / 256)),
+                    32 * kJoinGroups, 0, 0, s, pairs, static_cast<const float*>(part), scale, dE, static_cast<int>(M), V,
+                    static_cast<int>(D), w.chunk, w.items, accumulate ? 1 : 0);
+}
+
+coda_status_t coda_add_rmsnorm_mx(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float eps,
+                                  uint16_t* h_out, uint8_t* yq_out, uint8_t* ysf_out, float* r_out, int64_t M,
+                                  int64_t N, void* stream) {
+  CODA_CHECK(M >= 0 && M <= kMaxInt - 127 && dim_ok(N) && N % 128 == 0 && N <= kNorm8MaxN && eps >= 0.f,
+             CODA_ERR_SHAPE);
+  CODA_CHECK(x && gamma && yq_out && ysf_out, CODA_ERR_NULL);
+  CODA_CHECK(al16(x) && al16(res) && al16(gamma) && al16(h_out) && al16(yq_out) && al16(ysf_out) && al16(r_out),
+             CODA_ERR_ALIGN);
+  if (M == 0) return CODA_OK;
+  int dev;
+  DevInfo* info;
+  const coda_status_t st = current_device(&dev, &info);
+  if (st != CODA_OK) return st;
+  return launch_norm8<true>(x, res, gamma, eps, nullptr, h_out, yq_out, ysf_out, nullptr, r_out, M, N,
+                            static_cast<cudaStream_t>(stream));
+}
+
+coda_status_t coda_add_rmsnorm_fp8(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float eps,
+                                   const float* s_y, uint16_t* h_out, uint8_t* y8_out, float* amax_out, float* r_out,
+                                   int64_t M, int64_t N, void* stream) {
+  CODA_CHECK(M >= 0 && M <= kMaxInt && dim_ok(N) && N % 16 == 0 && N <= kNorm8MaxN && eps >= 0.f, CODA_ERR_SHAPE);
+  CODA_CHECK(x && gamma && s_y && y8_out && amax_out, CODA_ERR_NULL);
+  CODA_CHECK(al16(x) && al16(res) && al16(gamma) && al16(s_y) && al16(h_out) && al16(y8_out) && al16(amax_out) &&
+                 al16(r_out),
+             CODA_ERR_ALIGN);
+  if (M == 0) return CODA_OK;
+  int dev;
+  DevInfo* info;
+  const coda_status_t st = current_device(&dev, &info);
+  if (st != CODA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M > 1 && cudaMemsetAsync(amax_out, 0, sizeof(float), s) != cudaSuccess) return CODA_ERR_LAUNCH;
+  return launch_norm8<false>(x, res, gamma, eps, s_y, h_out, y8_out, nullptr, reinterpret_cast<unsigned*>(amax_out),
+                             r_out, M, N, s);
+}
+
+size_t coda_add_rmsnorm_bwd_workspace_size(int64_t M, int64_t N) {
+  if (M <= 0 || !dim_ok(N) || N > kNorm8MaxN) return 0;
+  return static_cast<size_t>(norm8_bwd_blocks(M, N)) * N * 4;
+}
+
+coda_status_t coda_add_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const float* r, const uint16_t* gamma,
+                                   const uint16_t* d_h, uint16_t* dx_out, float* dgamma_out, void* ws,
+                                   size_t ws_bytes, int64_t M, int64_t N, void* stream) {
+  CODA_CHECK(M >= 0 && M <= kMaxInt && dim_ok(N) && N <= kNorm8MaxN, CODA_ERR_SHAPE);
+  CODA_CHECK(dgamma_out && (M == 0 || (dy && h && r && gamma && dx_out)), CODA_ERR_NULL);
+  CODA_CHECK(al16(dy) && al16(h) && al16(r) && al16(gamma) && al16(d_h) && al16(dx_out) && al16(dgamma_out) &&
+                 al16(ws),
+             CODA_ERR_ALIGN);
+  CODA_CHECK(M == 0 || (ws && ws_bytes >= coda_add_rmsnorm_bwd_workspace_size(M, N)), CODA_ERR_WORKSPACE);
+  int dev;
+  DevInfo* info;
+  coda_status_t st = current_device(&dev, &info);
+  if (st != CODA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0)
+    return cudaMemsetAsync(dgamma_out, 0, static_cast<size_t>(N) * 4, s) == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
+  const int blocks = norm8_bwd_blocks(M, N);
+  const int threads = norm8_threads(N);
+  auto kern = norm8_vpt(N) == 1 ? add_rmsnorm_bwd_kernel<1, 64>
+                                : (threads <= 512 ? add_rmsnorm_bwd_kernel<2, 512> : add_rmsnorm_bwd_kernel<2, 1024>);
+  st = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), threads, 0, 0, s,
+                  reinterpret_cast<const __nv_bfloat16*>(dy), reinterpret_cast<const __nv_bfloat16*>(h), r,
+                  reinterpret_cast<const __nv_bfloat16*>(gamma), reinterpret_cast<const __nv_bfloat16*>(d_h),
+                  reinterpret_cast<__nv_bfloat16*>(dx_out), static_cast<float*>(ws), M, static_cast<int>(N));
+  if (st != CODA_OK) return st;
+  dgamma_final_kernel<<<static_cast<unsigned>((N + kDgCols - 1) / kDgCols), kDgCols * kDgGroups, 0, s>>>(
+      static_cast<const float*>(ws), blocks, static_cast<int>(N), dgamma_out);
+  return cudaGetLastError() == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
+}
+
+size_t coda_newton_schulz_workspace_size(int64_t batch, int64_t m, int64_t n) {
+  if (batch <= 0 || !dim_ok(m) || !dim_ok(n)) return 0;
+  return ns_plan(batch, m, n).bytes;
+}
+
+coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, int64_t m, int64_t n, int steps, float a,
+                                 float b, float c, float eps, void* ws, size_t ws_bytes, void* stream) {
+  CODA_CHECK(batch >= 0 && batch <= 65535 && dim_ok(m) && dim_ok(n) && steps >= 1 && steps <= 100 && eps >= 0.f,
+             CODA_ERR_SHAPE);
+  CODA_CHECK(m * n <= int64_t(1) << 38, CODA_ERR_SHAPE);  // byte strides of the tensor maps
+  CODA_CHECK(G && out, CODA_ERR_NULL);
+  CODA_CHECK(al16(G) && al16(out) && al16(ws), CODA_ERR_ALIGN);
+  if (batch == 0) return CODA_OK;
+  const NsPlan pl = ns_plan(batch, m, n);
+  CODA_CHECK(ws && ws_bytes >= pl.bytes, CODA_ERR_WORKSPACE);
+  const int64_t rt = (m + 127) / 128, ct = (n + 127) / 128;
+  CODA_CHECK(batch * rt * ct <= kMaxInt, CODA_ERR_SHAPE);
+  int dev;
+  DevInfo* info;
+  coda_status_t st = current_device(&dev, &info);
+  if (st != CODA_OK) return st;
+  cudaStream_t stm = static_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  __half* hi[2] = {reinterpret_cast<__half*>(w + pl.hi[0]), reinterpret_cast<__half*>(w + pl.hi[1])};
+  __half* lo[2] = {reinterpret_cast<__half*>(w + pl.lo[0]), reinterpret_cast<__half*>(w + pl.lo[1])};
+  __half* A = reinterpret_cast<__half*>(w + pl.A);
+  __half* B = reinterpret_cast<__half*>(w + pl.B);
+  float* dA = reinterpret_cast<float*>(w + pl.dA);
+  float* dB = reinterpret_cast<float*>(w + pl.dB);
+  double* part = reinterpret_cast<double*>(w + pl.part);
+  const size_t n8 = static_cast<size_t>(m) * n / 8;
+  st = launch_pdl(ns_sumsq_kernel, dim3(static_cast<unsigned>(pl.norm_blocks), static_cast<unsigned>(batch)),
+                  kNsNormThreads, 0, 0, stm, G, n8, pl.norm_blocks, part);
+  if (st != CODA_OK) return st;
+  st = launch_pdl(ns_scale_kernel, dim3(static_cast<unsigned>(pl.norm_blocks), static_cast<unsigned>(batch)),
+                  kNsNormThreads, 0, 0, stm, G, n8, pl.norm_blocks, static_cast<const double*>(part),
+                  static_cast<double>(eps), hi[0], steps > 1 ? lo[0] : static_cast<__half*>(nullptr));
+  if (st != CODA_OK) return st;
+  const int64_t s = pl.s, l = pl.tall ? m : n;  // smaller and larger side
+  NsParams gr{}, sq{}, up{};
+  gr.batch = sq.batch = up.batch = static_cast<int>(batch);
+  gr.sym_block = sq.sym_block = up.sym_block = pl.block;
+  gr.a = sq.a = up.a = a;
+  gr.b = sq.b = up.b = b;
+  gr.c = sq.c = up.c = c;
+  gr.rows = gr.cols = sq.rows = sq.cols = sq.K = static_cast<int>(s);
+  gr.K = static_cast<int>(l);
+  gr.d_out = dA;
+  sq.in0 = A;
+  sq.d_in = dA;
+  sq.d_out = dB;
+  up.rows = static_cast<int>(m);
+  up.cols = static_cast<int>(n);
+  up.K = static_cast<int>(s);
+  up.d_in = dB;
+  up.tall = pl.tall ? 1 : 0;
+  bool ok = ns_operand(&sq.P, A, kNsSym, s, s, batch) && tmap3d(&gr.out0, A, false, s, s, batch, 32) &&
+            tmap3d(&sq.out0, B, false, s, s, batch, 32);
+  sq.Q = sq.P;
+  for (int k = 0; ok && k < steps; ++k) {
+    const __half* x = hi[k & 1];
+    const bool last = k + 1 == steps;
+    // X [m, n]: for X X^T its rows are the operands' rows; for X^T X its columns
+    ok = ns_operand(&gr.P, x, pl.tall ? kNsMN : kNsK, s, l, batch);
+    gr.Q = gr.P;
+    if (pl.tall)
+      ok = ok && ns_operand(&up.P, x, kNsK, m, s, batch) && ns_operand(&up.Q, B, kNsSym, s, s, batch);
+    else
+      ok = ok && ns_operand(&up.P, B, kNsSym, s, s, batch) && ns_operand(&up.Q, x, kNsMN, n, s, batch);
+    up.in0 = x;
+    up.in1 = last ? nullptr : lo[k & 1];
+    up.last = last ? 1 : 0;
+    up.has_low = k + 2 < steps ? 1 : 0;
+    ok = ok && (last ? tmap3d(&up.out0, out, true, n, m, batch, 32)
+                     : tmap3d(&up.out0, hi[(k + 1) & 1], false, n, m, batch, 32));
+    ok = ok && (!up.has_low || tmap3d(&up.out1, lo[(k + 1) & 1], false, n, m, batch, 32));
+    if (!ok) return CODA_ERR_INTERNAL;
+    st = pl.block == 256 ? ns_launch<kNsGram, true>(dev, info, gr, stm) : ns_launch<kNsGram, false>(dev, info, gr, stm);
+    if (st != CODA_OK) return st;
+    st = pl.block == 256 ? ns_launch<kNsSquare, true>(dev, info, sq, stm)
+                         : ns_launch<kNsSquare, false>(dev, info, sq, stm);
+    if (st != CODA_OK) return st;
+    st = pl.pair_up ? ns_launch<kNsUpdate, true>(dev, info, up, stm) : ns_launch<kNsUpdate, false>(dev, info, up, stm);
+    if (st != CODA_OK) return st;
+  }
+  return ok ? CODA_OK : CODA_ERR_INTERNAL;
+}
+
+}  // extern "C"

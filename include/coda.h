@@ -486,6 +486,91 @@ coda_status_t coda_gemm_rowscale_partial_mx(const uint8_t* Aq, const uint8_t* As
                                             float eps, float* r_out, uint16_t* out, int64_t M, int64_t N, int64_t K,
                                             void* stream);
 
+/* ------------------------------------------- around the GEMM chain
+ *
+ * The rest of a training step on the same tensors: the token embedding before
+ * the first norm and its gradient, a residual add + RMSNorm that hands 8-bit
+ * operands to the FP8 and MXFP8 GEMMs (where no GEMM epilogue precedes the
+ * norm) with its backward, and the orthogonalised update of a weight from its
+ * fp32 gradient.  The article does not cover them.  Kernels are launched with
+ * programmatic stream serialisation, as the GEMMs; every call can be captured
+ * into a CUDA graph. */
+
+/* Token embedding: h = scale * E[token] (fp32 product), then what the first
+ * norm of the GEMM chain needs, as coda_gemm_res_partialrms writes it:
+ *   h_out = bf16(h), hg_out = bf16(gamma * h)   [M, D]
+ *   partial[t, i] = sum over the 128-column slot t of h_ij^2 (unrounded h) [T, M] fp32
+ * Outputs may be NULL, not all three; hg_out needs gamma.  tokens [M] int64; a
+ * token outside [0, V) (padding) gives a zero row.  E [V, D], gamma [D] bf16. */
+coda_status_t coda_embed(const int64_t* tokens, const uint16_t* E, float scale, const uint16_t* gamma, uint16_t* h_out,
+                         uint16_t* hg_out, float* partial, int64_t M, int64_t D, int64_t V, void* stream);
+
+/* Bytes of workspace coda_embed_bwd needs (0 for M <= 0): the sorted (token,
+ * row) pairs and the sums of runs that cross a block's border. */
+size_t coda_embed_bwd_workspace_size(int64_t M, int64_t D);
+
+/* Gradient of coda_embed's h: dE[v] = scale * sum over i with tokens[i] = v of
+ * dh_i, in fp32 with increasing i within blocks of fixed size (the same bits
+ * from call to call, however often a token occurs).  accumulate = 0: every row
+ * of dE is written (zero where the token does not occur); accumulate != 0: the
+ * sums are added to dE, whose other rows are not touched.  Tokens outside
+ * [0, V) contribute nothing.  dh [M, D] bf16, dE [V, D] fp32.  M == 0 zeroes
+ * dE or, accumulating, does nothing. */
+coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float scale, float* dE, int accumulate, void* ws,
+                             size_t ws_bytes, int64_t M, int64_t D, int64_t V, void* stream);
+
+/* Residual add + RMSNorm with an MXFP8 output for coda_gemm_rowscale_partial_mx
+ * (partial NULL): h = x + res (res NULL: h = x), r_i = 1 / sqrt(mean_j h_ij^2 +
+ * eps) from the unrounded h, y = gamma * h * r; h_out = bf16(h) (or NULL),
+ * yq_out [M, N] the e4m3 codes of y per 32 columns and ysf_out their scales in
+ * the A layout (coda_mx_sf_bytes(M, N, 0) bytes, padding rows 127), both as
+ * coda_mx_quantize forms them but from the fp32 y; r_out [M] fp32 or NULL.
+ * N a multiple of 128, at most 16384. */
+coda_status_t coda_add_rmsnorm_mx(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float eps,
+                                  uint16_t* h_out, uint8_t* yq_out, uint8_t* ysf_out, float* r_out, int64_t M,
+                                  int64_t N, void* stream);
+
+/* The same with per-tensor e4m3 codes for coda_gemm_fp8: y8_out = e4m3(y /
+ * s_y) [M, N] (saturating; s_y a device float, from an earlier call's amax by
+ * coda_fp8_scale_from_amax) and amax_out = max |y| (a device float; NaNs are
+ * left out; not written when M == 0).  N a multiple of 16, at most 16384. */
+coda_status_t coda_add_rmsnorm_fp8(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float eps,
+                                   const float* s_y, uint16_t* h_out, uint8_t* y8_out, float* amax_out, float* r_out,
+                                   int64_t M, int64_t N, void* stream);
+
+/* Bytes of workspace coda_add_rmsnorm_bwd needs (per-block dgamma sums; 0 for M <= 0). */
+size_t coda_add_rmsnorm_bwd_workspace_size(int64_t M, int64_t N);
+
+/* Backward of both (the codes' rounding counts as the identity): with
+ * g = dy * gamma,  dx_i = r_i g_i - r_i^3 mean_j(g_ij h_ij) h_i + d_h_i,
+ * dgamma_j = sum_i dy_ij h_ij r_i (fixed order).  dx is the gradient of x and
+ * of res.  d_h [M, N] bf16 or NULL: the gradient that reaches h by the
+ * residual stream.  dy, h [M, N], gamma [N] bf16, r [M] fp32; dx_out [M, N]
+ * bf16, dgamma_out [N] fp32.  N a multiple of 8, at most 16384.  M == 0 zeroes
+ * dgamma. */
+coda_status_t coda_add_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const float* r, const uint16_t* gamma,
+                                   const uint16_t* d_h, uint16_t* dx_out, float* dgamma_out, void* ws,
+                                   size_t ws_bytes, int64_t M, int64_t N, void* stream);
+
+/* Bytes of workspace coda_newton_schulz needs (0 for a bad shape): X twice in
+ * two fp16 parts, and two square fp16 matrices of the smaller side. */
+size_t coda_newton_schulz_workspace_size(int64_t batch, int64_t m, int64_t n);
+
+/* Newton-Schulz orthogonalisation of `batch` matrices (the step of the Muon
+ * optimiser): X = G / (|G|_F + eps), then `steps` times
+ *   A = X X^T;  X <- a X + (b A + c A^2) X      (X^T X and the other side if m > n)
+ * and out = bf16(X).  G [batch, m, n] fp32 (a gradient or momentum, such as the
+ * backward calls give), out [batch, m, n] bf16.  The products take fp16
+ * operands with fp32 sums and corrections for their rounding: about 1e-3 of
+ * |X|_F from exact arithmetic before the output's rounding.  The coefficients
+ * must keep the singular values bounded, as Muon's (3.4445, -4.775, 2.0315)
+ * do: intermediate values beyond 16 (X) or 64 (A, b A + c A^2) become
+ * infinite.  A matrix with a non-finite entry gives a non-finite result and
+ * leaves the others of the batch alone; a zero matrix gives zeros if eps > 0.
+ * m and n multiples of 8, m * n <= 2^38, 1 <= steps <= 100, batch <= 65535. */
+coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, int64_t m, int64_t n, int steps, float a,
+                                 float b, float c, float eps, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- testing */
 
 /* Launches one block that waits on a barrier nothing ever signals, with time
