@@ -52,43 +52,41 @@ constexpr float kNsScaleX = 4096.f;
 constexpr float kNsScaleA = 1024.f;
 constexpr float kNsScaleB = 1024.f;
 
-constexpr int kNsThreads = 192;  // TMA producer, MMA issuer, four epilogue warps
-constexpr int kNsEpiWarps = 4;
-constexpr int kNsStages = 6;
+constexpr int kNsEpiWarps = 8;                     // two per TMEM lane quarter, each half of a tile's columns
+constexpr int kNsThreads = 64 + 32 * kNsEpiWarps;  // TMA producer, MMA issuer, epilogue warps
+constexpr int kNsStages = 5;
 constexpr int kNsOpBytes = 128 * 64 * 2;  // one operand's 128 rows of a 64-wide k-block
 constexpr int kNsStageBytes = 2 * kNsOpBytes;
-constexpr int kNsEpiBytes = 8192;  // staging per epilogue warp: two 32 x 64 fp16 boxes
-constexpr int kNsBars = 2 * kNsStages + 2 + 2 + 1;
-constexpr int kNsSmemBytes = 1024 + kNsStages * kNsStageBytes + kNsEpiWarps * kNsEpiBytes + kNsBars * 8 + 16;
+constexpr int kNsBoxBytes = 32 * 32 * 2;      // a 32 x 32 box of an epilogue
+constexpr int kNsEpiBytes = 4 * kNsBoxBytes;  // per epilogue warp: two buffers of a high and a low box
+constexpr int kNsBars = 2 * kNsStages + 2 + 2 + 1 + 1 + 2 * kNsEpiWarps;
+constexpr int kNsSmemBytes = 1024 + kNsStages * kNsStageBytes + kNsEpiWarps * kNsEpiBytes + kNsBars * 8 + 32;
 static_assert(kNsSmemBytes <= 232448, "shared memory");
 
 enum NsKind : int { kNsGram = 0, kNsSquare, kNsUpdate };
 
-// How an operand's 128 rows (of the output's rows or columns) by 64 k of a
-// k-block are found: stored [row, k], stored [k, row], or in a symmetric matrix
-// of which the blocks (of `sym_block`) on and below the diagonal are stored.
-enum NsMajor : int { kNsK = 0, kNsMN, kNsSym };
-
-struct NsOperand {
-  CUtensorMap k;   // [batch, row, k], box 128 rows x 64 k
-  CUtensorMap mn;  // [batch, k, row], box 64 k x 64 rows
-  int major;
+// One of the three GEMMs, acc[i, j] = sum_k P[i, k] Q[j, k], over the batch.
+struct NsGeo {
+  int rows, cols, nkb;    // output size of one matrix, 64-wide k-blocks
+  int n_rt, n_ct, tiles;  // row tiles, column tiles, tiles of one matrix (half of them for a symmetric result)
+  int whole;              // the first `whole` tiles of the batch are one unit each,
+  int rest;               // the other `rest` tiles
+  int splits;             // are `splits` units each, over equal shares of the k-blocks
 };
 
 struct NsParams {
-  NsOperand P, Q;          // acc[i, j] = sum_k P[i, k] Q[j, k]
-  CUtensorMap out0, out1;  // stores, box 32 rows x 64 columns: result (high part), low part
-  const __half* in0;       // epilogue input of the output's shape: A (square), X high (update)
-  const __half* in1;       // X low (update), or null
-  const float* d_in;       // dA [batch, rows] (square), dB (update)
-  float* d_out;            // dA (gram), dB (square): what fp16 drops of the diagonal
-  int rows, cols, K, batch;
-  int n_rt, n_ct, tiles;   // row tiles, column tiles, tiles of one matrix
-  int sym_block;
-  int tall;                // update: X B (dB goes with the columns)
-  int last;                // update: the result is the bf16 output
-  int has_low;             // update: the result's low part is stored
-  float a, b, c;           // coefficients
+  // loads, 3-D [batch, y, x] with 64-wide boxes: 128 rows (K-major operand) or 64 k (MN-major)
+  CUtensorMap Xk[2], Xmn[2];  // X's high part, by step parity
+  CUtensorMap Ak, Amn, Bk, Bmn;
+  // the epilogues' boxes of 32 x 32 (64-byte swizzle): X's high and low parts, A, B, the output
+  CUtensorMap Hbox[2], Lbox[2], Abox, Bbox, Obox;
+  float* dA;  // [batch, s]: what fp16 drops of A's diagonal
+  float* dB;
+  float* part;    // partial accumulators of the split tiles
+  int* counters;  // [0]: arrivals at the grid barrier; then for each GEMM arrivals at the split tiles' parts
+  NsGeo geo[3];
+  int batch, steps, tall;
+  float a, b, c;
   uint64_t wait_ns;
 };
 
@@ -133,39 +131,313 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// Whether the k-block at k0 of an operand's rows at row0 is loaded [k, row].
-__device__ __forceinline__ bool ns_is_mn(int major, int row0, int k0, int sym_block) {
-  return major == kNsMN || (major == kNsSym && k0 / sym_block > row0 / sym_block);
-}
+// A unit of work: a tile (matrix, row tile, column tile) and its k-blocks.
+struct NsUnit {
+  int bz, rt, ct;
+  int kb0, kb1;
+  int part;   // which of a split tile's parts (-1: a whole tile)
+  int split;  // the split tile's number
+};
 
-// Unit u -> matrix, row tile, column tile.  A symmetric result takes the tiles
-// on and below the diagonal, row by row: row i starts at tile i (i + 1) / 2.
+// A symmetric result takes the tiles on and below the diagonal, row by row: row
+// i starts at tile i (i + 1) / 2.  Otherwise the tiles that share the longer
+// side's operand follow each other.
 template <bool SYM>
-__device__ __forceinline__ void ns_map(const NsParams& p, int u, int& bz, int& rt, int& ct) {
-  bz = u / p.tiles;
-  const int t = u - bz * p.tiles;
+__device__ __forceinline__ NsUnit ns_unit(const NsGeo& g, int u) {
+  NsUnit n;
+  int t = u;
+  n.part = -1;
+  n.split = 0;
+  n.kb0 = 0;
+  n.kb1 = g.nkb;
+  if (u >= g.whole) {
+    n.split = (u - g.whole) / g.splits;
+    const int k = (u - g.whole) - n.split * g.splits;
+    t = g.whole + n.split;
+    if (g.splits > 1) {
+      n.part = k;
+      n.kb0 = g.nkb * k / g.splits;
+      n.kb1 = g.nkb * (k + 1) / g.splits;
+    }
+  }
+  n.bz = t / g.tiles;
+  t -= n.bz * g.tiles;
   if (SYM) {
     int i = static_cast<int>((sqrtf(8.f * static_cast<float>(t) + 1.f) - 1.f) * 0.5f);
     while (i * (i + 1) / 2 > t) --i;
     while ((i + 1) * (i + 2) / 2 <= t) ++i;
-    rt = i;
-    ct = t - i * (i + 1) / 2;
-  } else if (p.n_rt <= p.n_ct) {  // the tiles that share the longer side's operand follow each other
-    ct = t / p.n_rt;
-    rt = t - ct * p.n_rt;
+    n.rt = i;
+    n.ct = t - i * (i + 1) / 2;
+  } else if (g.n_rt <= g.n_ct) {
+    n.ct = t / g.n_rt;
+    n.rt = t - n.ct * g.n_rt;
   } else {
-    rt = t / p.n_ct;
-    ct = t - rt * p.n_ct;
+    n.rt = t / g.n_ct;
+    n.ct = t - n.rt * g.n_ct;
+  }
+  return n;
+}
+
+__device__ __forceinline__ NsUnit ns_unit(const NsParams& p, int kind, int u) {
+  return kind == kNsUpdate ? ns_unit<false>(p.geo[kind], u) : ns_unit<true>(p.geo[kind], u);
+}
+
+// An operand of one GEMM: its two views, and whether the k-block at k0 of the
+// rows of tile `t` is loaded [k, row] (the MN-major view).
+struct NsOperand {
+  const CUtensorMap *k, *mn;
+  int sym;  // A or B: blocks of the tile's size on and below the diagonal are stored
+  __device__ __forceinline__ bool is_mn(int t, int kb, int tile) const { return sym ? kb * 64 / tile > t : mn != nullptr; }
+};
+
+__device__ __forceinline__ void ns_operands(const NsParams& p, int kind, int par, NsOperand& P, NsOperand& Q) {
+  const NsOperand xk{&p.Xk[par], nullptr, 0}, xm{nullptr, &p.Xmn[par], 0};
+  if (kind == kNsGram) {
+    P = Q = p.tall ? xm : xk;
+  } else if (kind == kNsSquare) {
+    P = Q = NsOperand{&p.Ak, &p.Amn, 1};
+  } else {
+    const NsOperand bs{&p.Bk, &p.Bmn, 1};
+    P = p.tall ? xk : bs;
+    Q = p.tall ? bs : xm;
   }
 }
 
+// Byte offset of 16-byte chunk `chunk` (0..3) of row `row` in a box of 64-byte
+// rows with the 64-byte swizzle (base aligned to 512 bytes).
+__device__ __forceinline__ uint32_t sw64_off(int row, int chunk) {
+  return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+}
+
+constexpr int kNsSplitCounters = 74 * 16;  // of one GEMM: split tiles (at most half of the slots) x warps
+
+// What an epilogue warp keeps.
+struct NsEpi {
+  uint8_t* stg;       // its two buffers
+  uint64_t* bars;     // a barrier for each, for the loads
+  uint32_t taddr;     // TMEM address of its lanes, first accumulator
+  int rank, q, half;  // CTA of the pair, lane quarter, half of the columns
+  int lane;
+  uint32_t cnt;       // blocks done: block i uses buffer i & 1
+  uint32_t loads;     // bit i: parity of buffer i's next load
+};
+
+// v[4 j ..] += o
+__device__ __forceinline__ void ns_add4(uint32_t (&v)[32], int j, const float4& o) {
+  v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + o.x);
+  v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + o.y);
+  v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + o.z);
+  v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + o.w);
+}
+
+// One unit's epilogue for one warp: 32 rows x half of the tile's columns, in
+// blocks of 32 columns (a thread has one row).  A block's inputs come by TMA
+// into a staging buffer, one block ahead; the thread replaces its row by the
+// results, which leave by TMA from the same buffer.  (Direct loads of a row per
+// thread touch 32 lines an instruction and bound the update at 20 us a tile.)
+// The loop over blocks is not unrolled: three epilogues alternate in this
+// kernel, and straight-line code that runs once per GEMM is bound by
+// instruction fetches.  Returns false if a wait gave up.
+template <int KIND, bool PAIR>
+__device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, int k, int acc, uint32_t parity,
+                                            uint64_t* tfull, NsEpi& e, const WaitCtx& w) {
+  constexpr int kTile = PAIR ? 256 : 128;
+  constexpr int kHalf = kTile / 2;    // columns of this warp
+  constexpr int kBlks = kHalf / 32;
+  const NsGeo& g = p.geo[KIND];
+  const bool last = k + 1 == p.steps;
+  const bool has_low = KIND == kNsUpdate && k + 2 < p.steps;  // the result's low part is stored
+  const bool in_low = KIND == kNsUpdate && !last;             // X has one
+  const CUtensorMap* in0 = KIND == kNsSquare ? &p.Abox : &p.Hbox[k & 1];
+  const CUtensorMap* in1 = &p.Lbox[k & 1];
+  const int lane = e.lane;
+  const int row0 = n.rt * kTile + e.rank * 128 + e.q * 32;
+  const int row = row0 + lane;
+  const int col0 = n.ct * kTile + e.half * kHalf;
+  const bool live = row < g.rows;
+  // dA (square: of the row and of the column), dB (update: of the row of B X, of the column of X B)
+  const bool by_col = KIND == kNsSquare || (KIND == kNsUpdate && p.tall);
+  const float* dv = (KIND == kNsSquare ? p.dA : p.dB) + static_cast<size_t>(n.bz) * (by_col ? g.cols : g.rows);
+  float di = 0.f;
+  if (KIND == kNsSquare || (KIND == kNsUpdate && !by_col)) di = live ? __ldcg(dv + row) : 0.f;
+  int nblk = (g.cols - col0 + 31) / 32;
+  if (nblk > kBlks) nblk = kBlks;
+  if (row0 >= g.rows || nblk < 0) nblk = 0;  // (uniform over the warp)
+  // the blocks this warp finishes: all, or of a split tile this part's share
+  int b0 = 0, b1 = nblk;
+  if (n.part >= 0) {
+    b0 = n.part * (kBlks / g.splits);
+    b1 = min(nblk, b0 + kBlks / g.splits);
+  }
+  float dc = 0.f;  // d of the block's column number `lane`
+  auto fetch = [&](int b, uint32_t cnt) {
+    if (KIND == kNsGram) return;
+    const int c = col0 + b * 32;
+    if (lane == 0) {
+      bulk_wait_read<0>();  // the buffer's last store has left it
+      uint8_t* d = e.stg + (cnt & 1) * (2 * kNsBoxBytes);
+      mbar_arrive_expect_tx(&e.bars[cnt & 1], in_low ? 2 * kNsBoxBytes : kNsBoxBytes);
+      tma_load_3d(d, in0, &e.bars[cnt & 1], c, row0, n.bz);
+      if (in_low) tma_load_3d(d + kNsBoxBytes, in1, &e.bars[cnt & 1], c, row0, n.bz);
+    }
+    if (by_col) dc = c + lane < g.cols ? __ldcg(dv + c + lane) : 0.f;
+  };
+  if (b0 < b1) fetch(b0, e.cnt);
+  // Warp-uniform outcomes: tcgen05.ld below is a warp-collective instruction.
+  if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], parity, w))) return false;
+  tc_fence_after();
+  const uint32_t taddr = e.taddr + acc * kTile + e.half * kHalf;
+  // A split tile: each part hands the others' blocks of its accumulator over
+  // through memory, waits for theirs and adds up the parts of its own blocks in
+  // an order that does not depend on whose they are.  The parts run at the same time (they are the last units of
+  // their CTAs in this GEMM).  A lane's float4 lie 512 bytes apart, so a warp's
+  // access is contiguous.
+  constexpr size_t kPart = static_cast<size_t>(PAIR ? 16 : 8) * 32 * kHalf / 4;  // float4 of a tile's part
+  float4* part = nullptr;
+  if (n.part >= 0 && nblk > 0) {
+    const int region = (e.rank * 4 + e.q) * 2 + e.half;
+    part = reinterpret_cast<float4*>(p.part) + static_cast<size_t>(n.split) * g.splits * kPart +
+           region * (32 * kHalf / 4) + lane;
+#pragma unroll 1
+    for (int b = 0; b < nblk; ++b) {
+      if (b >= b0 && b < b1) continue;
+      uint32_t v[32];
+      tmem_ld32(taddr + b * 32, v);
+      tmem_ld_wait(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        __stcg(part + n.part * kPart + (b * 8 + j) * 32,
+               make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]), __uint_as_float(v[4 * j + 2]),
+                           __uint_as_float(v[4 * j + 3])));
+    }
+    __threadfence();
+    __syncwarp();
+    int ok = 1;
+    if (lane == 0) {
+      int* c = p.counters + 1 + KIND * kNsSplitCounters + n.split * (PAIR ? 16 : 8) + region;
+      red_release_add(c, 1);
+      if (b0 < b1) ok = counter_wait(c, g.splits * (k + 1), w) ? 1 : 0;
+      __threadfence();
+    }
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+  }
+  const int dcol = KIND != kNsUpdate && n.rt == n.ct ? row : -1;  // this row's diagonal column, if the tile has it
+  float dval = 0.f;                                               // the value there
+  // the accumulator's share: gram S_A / S_X^2, square c S_B / S_A^2, update 1 / S_B
+  const float sc = KIND == kNsGram ? kNsScaleA / (kNsScaleX * kNsScaleX)
+                                   : (KIND == kNsSquare ? p.c * (kNsScaleB / (kNsScaleA * kNsScaleA)) : 1.f / kNsScaleB);
+  // on the diagonal the square has b d + c d^2 more: (A + D)^2 = A^2 + D A + A D + D^2
+  const float corr = KIND == kNsSquare ? di * fmaf(p.c, di, p.b) * kNsScaleB : 0.f;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b, ++e.cnt) {
+    const int c32 = col0 + b * 32;
+    const int buf = e.cnt & 1;
+    uint8_t* S0 = e.stg + buf * (2 * kNsBoxBytes);
+    uint8_t* S1 = S0 + kNsBoxBytes;
+    const float dcb = dc;
+    if (KIND == kNsGram) {
+      if (lane == 0) bulk_wait_read<1>();
+      __syncwarp();
+    } else {
+      if (b + 1 < b1) fetch(b + 1, e.cnt + 1);
+      if (!__all_sync(0xffffffffu, mbar_wait(&e.bars[buf], (e.loads >> buf) & 1, w))) return false;
+      e.loads ^= 1u << buf;
+    }
+    uint32_t v[32];
+    tmem_ld32(taddr + b * 32, v);
+    tmem_ld_wait(v);
+    if (part != nullptr) {
+      // (p0 + p1), or (p0 + p1) + (p2 + p3): own and partner first, then the other pair
+      const float4* f = part + b * 256;
+      float4 o[8], q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = __ldcg(f + (n.part ^ 1) * kPart + j * 32);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ns_add4(v, j, o[j]);
+      if (g.splits == 4) {
+        f += ((n.part ^ 2) & 2) * kPart;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j] = __ldcg(f + j * 32);
+          q[j] = __ldcg(f + kPart + j * 32);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          ns_add4(v, j, make_float4(o[j].x + q[j].x, o[j].y + q[j].y, o[j].z + q[j].z, o[j].w + q[j].w));
+      }
+    }
+    const bool bf_out = KIND == kNsUpdate && last;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t off = sw64_off(lane, j);
+      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = make_uint4(0, 0, 0, 0);
+      if (KIND != kNsGram) x0 = ld_shared_v4(S0 + off);
+      if (in_low) x1 = ld_shared_v4(S1 + off);
+      const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+      uint32_t o0[4], o1[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float r[2];
+        const float2 h = unpack_f16x2(w0[i]);
+        const float2 l = unpack_f16x2(w1[i]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int at = j * 8 + 2 * i + u;
+          const float ac = __uint_as_float(v[at]);
+          const float f = u ? h.y : h.x;
+          const float d = by_col ? __shfl_sync(0xffffffffu, dcb, at) : 0.f;
+          if (KIND == kNsGram)
+            r[u] = ac * sc;
+          else if (KIND == kNsSquare)  // b A + c (d_i + d_j) A (stored with S_A, wanted with S_B) + c acc
+            r[u] = fmaf(ac, sc, f * fmaf(p.c, di + d, p.b) * (kNsScaleB / kNsScaleA));
+          else  // (a + d) X + acc
+            r[u] = fmaf(ac, sc, (p.a + (di + d)) * (f + (u ? l.y : l.x)));
+          if (KIND != kNsUpdate && c32 + at == dcol) {
+            r[u] += corr;
+            dval = r[u];
+          }
+        }
+        if (bf_out) {
+          o0[i] = pack_bf16x2(r[0] * (1.f / kNsScaleX), r[1] * (1.f / kNsScaleX));
+          o1[i] = 0;
+        } else {
+          o0[i] = pack_f16x2(r[0], r[1]);
+          const float2 hr = unpack_f16x2(o0[i]);
+          o1[i] = KIND == kNsUpdate ? pack_f16x2(r[0] - hr.x, r[1] - hr.y) : 0u;
+        }
+      }
+      st_shared_v4(S0 + off, make_uint4(o0[0], o0[1], o0[2], o0[3]));
+      if (has_low) st_shared_v4(S1 + off, make_uint4(o1[0], o1[1], o1[2], o1[3]));
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      const CUtensorMap* m = KIND == kNsGram ? &p.Abox
+                                             : (KIND == kNsSquare ? &p.Bbox : (last ? &p.Obox : &p.Hbox[(k + 1) & 1]));
+      tma_store_3d(m, S0, c32, row0, n.bz);
+      if (has_low) tma_store_3d(&p.Lbox[(k + 1) & 1], S1, c32, row0, n.bz);
+      bulk_commit();
+    }
+  }
+  if (KIND != kNsUpdate && live && dcol >= col0 + b0 * 32 && dcol < col0 + b1 * 32)
+    (KIND == kNsGram ? p.dA : p.dB)[static_cast<size_t>(n.bz) * g.rows + row] =
+        (dval - __half2float(__float2half_rn(dval))) * (KIND == kNsGram ? 1.f / kNsScaleA : 1.f / kNsScaleB);
+  return true;
+}
+
+// All steps in one persistent launch.  The CTAs (or CTA pairs) take the units of
+// a GEMM in turn; between two GEMMs all of them wait for each other at a counter
+// in global memory: a CTA arrives when the stores of its last epilogue warp have
+// completed; its producer thread polls the counter, loads on, and lets the
+// epilogue warps go on through an mbarrier.  All CTAs have to be resident at
+// once, so the launch is a cooperative one.
+//
 // PAIR: a cluster of two CTAs per 256 x 256 tile (cta_group::2, rank r owns
 // accumulator rows [128 r, 128 r + 128) and loads those rows of P and its half
 // of Q's); otherwise one CTA per 128 x 128 tile.
-template <int KIND, bool PAIR>
-__global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_constant__ NsParams p) {
+template <bool PAIR>
+__global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant__ NsParams p) {
   constexpr int kTile = PAIR ? 256 : 128;
-  constexpr bool kSymOut = KIND != kNsUpdate;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sEpi = smem + kNsStages * kNsStageBytes;
@@ -174,15 +446,19 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
   uint64_t* tfull = empty + kNsStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* go = drain + 1;  // the grid barrier after each GEMM, for this CTA's epilogue warps
+  uint64_t* ebars = go + 1;  // two for each epilogue warp
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(ebars + 2 * kNsEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* warps_done = reinterpret_cast<int*>(tmem_holder + 2);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const int step = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
   const int first = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
-  const int nunits = p.tiles * p.batch;
+  const int phases = 3 * p.steps;
+  const int arrivals = static_cast<int>(gridDim.x);  // per phase
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kNsStages; ++s) {
@@ -194,7 +470,10 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
       mbar_init(&tempty[a], PAIR ? 2 * kNsEpiWarps : kNsEpiWarps);
     }
     mbar_init(drain, 1);
+    mbar_init(go, 1);
+    for (int i = 0; i < 2 * kNsEpiWarps; ++i) mbar_init(&ebars[i], 1);
     *abort_flag = 0;
+    *warps_done = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -212,9 +491,6 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const WaitCtx w{abort_flag, p.wait_ns};
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int nkb = (p.K + 63) / 64;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -223,43 +499,51 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
       long issued = 0;
       bool ok = true;
       const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
-      for (int u = first; ok && u < nunits; u += step) {
-        int bz, rt, ct;
-        ns_map<kSymOut>(p, u, bz, rt, ct);
-        const int row0 = rt * kTile + rank * 128;
-        const int col0 = ct * kTile + rank * 128;
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
-            ok = false;
-            break;
-          }
-          if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * kNsStageBytes);
-          uint8_t* dst = smem + stage * kNsStageBytes;
-          const uint32_t fb = full0 + stage * 8;
+      for (int ph = 0; ok && ph < phases; ++ph) {
+        const int kind = ph % 3;
+        NsOperand op[2];
+        ns_operands(p, kind, (ph / 3) & 1, op[0], op[1]);
+        const int nunits = p.geo[kind].whole + p.geo[kind].rest * p.geo[kind].splits;
+        if (ph > 0) {
+          if (!counter_wait(p.counters, arrivals * ph, w)) break;
+          fence_proxy_async_global();  // the loads below see what other CTAs' copies wrote
+          mbar_arrive(go);
+        }
+        for (int u = first; ok && u < nunits; u += step) {
+          const NsUnit n = ns_unit(p, kind, u);
+          for (int kb = n.kb0; kb < n.kb1; ++kb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
+              ok = false;
+              break;
+            }
+            if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * kNsStageBytes);
+            uint8_t* dst = smem + stage * kNsStageBytes;
+            const uint32_t fb = full0 + stage * 8;
 #pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const NsOperand& op = o == 0 ? p.P : p.Q;
-            const int r0 = o == 0 ? row0 : col0;
-            uint8_t* d = dst + o * kNsOpBytes;
-            if (!ns_is_mn(op.major, r0, kb * 64, p.sym_block)) {
-              if (PAIR)
-                tma_load_3d_pair(d, &op.k, fb, kb * 64, r0, bz);
-              else
-                tma_load_3d(d, &op.k, &full[stage], kb * 64, r0, bz);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
+            for (int o = 0; o < 2; ++o) {
+              const int tile = o == 0 ? n.rt : n.ct;
+              const int r0 = tile * kTile + rank * 128;
+              uint8_t* d = dst + o * kNsOpBytes;
+              if (!op[o].is_mn(tile, kb, kTile)) {
                 if (PAIR)
-                  tma_load_3d_pair(d + j * 8192, &op.mn, fb, r0 + j * 64, kb * 64, bz);
+                  tma_load_3d_pair(d, op[o].k, fb, kb * 64, r0, n.bz);
                 else
-                  tma_load_3d(d + j * 8192, &op.mn, &full[stage], r0 + j * 64, kb * 64, bz);
+                  tma_load_3d(d, op[o].k, &full[stage], kb * 64, r0, n.bz);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  if (PAIR)
+                    tma_load_3d_pair(d + j * 8192, op[o].mn, fb, r0 + j * 64, kb * 64, n.bz);
+                  else
+                    tma_load_3d(d + j * 8192, op[o].mn, &full[stage], r0 + j * 64, kb * 64, n.bz);
+                }
               }
             }
-          }
-          ++issued;
-          if (++stage == kNsStages) {
-            stage = 0;
-            phase ^= 1u;
+            ++issued;
+            if (++stage == kNsStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
       }
@@ -283,49 +567,58 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
       uint32_t phase = 0;
       int it = 0;
       bool ok = true;
-      for (int u = first; ok && u < nunits; u += step, ++it) {
-        int bz, rt, ct;
-        ns_map<kSymOut>(p, u, bz, rt, ct);
-        const int acc = it & 1;
-        if (!mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, w)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + acc * kTile;
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(&full[stage], phase, w)) {
+      for (int ph = 0; ok && ph < phases; ++ph) {
+        const int kind = ph % 3;
+        NsOperand P, Q;
+        ns_operands(p, kind, (ph / 3) & 1, P, Q);
+        const int nunits = p.geo[kind].whole + p.geo[kind].rest * p.geo[kind].splits;
+        for (int u = first; ok && u < nunits; u += step, ++it) {
+          const NsUnit n = ns_unit(p, kind, u);
+          const int acc = it & 1;
+          if (!mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, w)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const bool pm = ns_is_mn(p.P.major, rt * kTile, kb * 64, p.sym_block);
-          const bool qm = ns_is_mn(p.Q.major, ct * kTile, kb * 64, p.sym_block);
-          const uint32_t idesc = idesc_f16_f32(kTile, kTile, pm, qm);
-          const uint32_t a0 = smem_u32(smem + stage * kNsStageBytes);
-          const uint32_t b0 = a0 + kNsOpBytes;
+          const uint32_t d = tmem_base + acc * kTile;
+          for (int kb = n.kb0; kb < n.kb1; ++kb) {
+            // between two GEMMs this waits as long as the slowest CTA works
+            if (!mbar_wait(&full[stage], phase, w)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const bool pm = P.is_mn(n.rt, kb, kTile);
+            const bool qm = Q.is_mn(n.ct, kb, kTile);
+            const uint32_t idesc = idesc_f16_f32(kTile, kTile, pm, qm);
+            const uint32_t a0 = smem_u32(smem + stage * kNsStageBytes);
+            const uint32_t b0 = a0 + kNsOpBytes;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ad = pm ? sdesc_sw128(a0 + kk * 2048, 8192, 1024) : sdesc_sw128(a0 + kk * 32, 16, 1024);
-            const uint64_t bd = qm ? sdesc_sw128(b0 + kk * 2048, 8192, 1024) : sdesc_sw128(b0 + kk * 32, 16, 1024);
-            const uint32_t accum = (kb | kk) ? 1u : 0u;
-            // (the kind::f16 instruction; the descriptor says fp16 operands)
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ad = pm ? sdesc_sw128(a0 + kk * 2048, 8192, 1024) : sdesc_sw128(a0 + kk * 32, 16, 1024);
+              const uint64_t bd = qm ? sdesc_sw128(b0 + kk * 2048, 8192, 1024) : sdesc_sw128(b0 + kk * 32, 16, 1024);
+              const uint32_t accum = (kb != n.kb0 || kk != 0) ? 1u : 0u;
+              // (the kind::f16 instruction; the descriptor says fp16 operands)
+              if (PAIR)
+                tc_mma_bf16_pair(d, ad, bd, idesc, accum);
+              else
+                tc_mma_bf16(d, ad, bd, idesc, accum);
+            }
             if (PAIR)
-              tc_mma_bf16_pair(d, ad, bd, idesc, accum);
+              tc_commit_pair_mc(&empty[stage], 0x3);
             else
-              tc_mma_bf16(d, ad, bd, idesc, accum);
+              tc_commit(&empty[stage]);
+            if (++stage == kNsStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
+          if (!ok) break;
           if (PAIR)
-            tc_commit_pair_mc(&empty[stage], 0x3);
+            tc_commit_pair_mc(&tfull[acc], 0x3);
           else
-            tc_commit(&empty[stage]);
-          if (++stage == kNsStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+            tc_commit(&tfull[acc]);
         }
-        if (!ok) break;
-        if (PAIR)
-          tc_commit_pair_mc(&tfull[acc], 0x3);
-        else
-          tc_commit(&tfull[acc]);
       }
       if (PAIR)
         tc_commit_pair(drain);
@@ -335,142 +628,58 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
       (void)mbar_wait(drain, 0, WaitCtx{&no_abort, p.wait_ns});
     }
   } else {
-    const int q = warp & 3;  // TMEM lane quarter this warp may access
-    uint8_t* stg = sEpi + (warp - 2) * kNsEpiBytes;
+    NsEpi e;
+    e.stg = sEpi + (warp - 2) * kNsEpiBytes;
+    e.q = warp & 3;  // the TMEM lane quarter this warp may access
+    e.half = (warp - 2) >> 2;
+    e.rank = rank;
+    e.lane = lane;
+    e.bars = ebars + 2 * (warp - 2);
+    e.cnt = 0;
+    e.loads = 0;
+    e.taddr = tmem_base + (static_cast<uint32_t>(e.q * 32) << 16);
     const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
-    uint32_t cnt = 0;
     int it = 0;
-    for (int u = first; u < nunits; u += step, ++it) {
-      int bz, rt, ct;
-      ns_map<kSymOut>(p, u, bz, rt, ct);
-      const int acc = it & 1;
-      const int row0 = rt * kTile + rank * 128 + q * 32;
-      const int row = row0 + lane;
-      const int col0 = ct * kTile;
-      const bool live = row < p.rows;
-      const size_t base = (static_cast<size_t>(bz) * p.rows + (live ? row : 0)) * p.cols;
-      const float* dv = KIND == kNsGram ? nullptr : p.d_in + static_cast<size_t>(bz) * (KIND == kNsUpdate && p.tall ? p.cols : p.rows);
-      const bool by_col = KIND == kNsSquare || (KIND == kNsUpdate && p.tall);
-      float di = 0.f;
-      if (KIND == kNsSquare || (KIND == kNsUpdate && !p.tall)) di = live ? __ldg(dv + row) : 0.f;
-      int nch = (p.cols - col0 + 63) / 64;
-      if (nch > kTile / 64) nch = kTile / 64;
-      if (row0 >= p.rows) nch = 0;  // (uniform over the warp)
-      uint4 x0[4], x1[4];
-      auto fetch = [&](int col) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x0[j] = make_uint4(0, 0, 0, 0);
-          x1[j] = make_uint4(0, 0, 0, 0);
-          if (KIND != kNsGram && live && col + j * 8 < p.cols) {
-            x0[j] = *reinterpret_cast<const uint4*>(p.in0 + base + col + j * 8);
-            if (KIND == kNsUpdate && p.in1 != nullptr)
-              x1[j] = *reinterpret_cast<const uint4*>(p.in1 + base + col + j * 8);
-          }
-        }
-      };
-      if (nch > 0) fetch(col0);
-      // Warp-uniform outcome: tcgen05.ld below is a warp-collective instruction.
-      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (it >> 1) & 1, w))) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kTile;
-      for (int ch = 0; ch < nch; ++ch) {
-        const int cc = col0 + ch * 64;
-        uint8_t* S0 = KIND == kNsUpdate ? stg : stg + (cnt & 1) * 4096;
-        uint8_t* S1 = stg + 4096;
-        if (lane == 0) {
-          if (KIND == kNsUpdate)
-            bulk_wait_read<0>();
-          else
-            bulk_wait_read<1>();
-        }
-        __syncwarp();
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int c32 = cc + hh * 32;
-          uint4 y0[4], y1[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            y0[j] = x0[j];
-            y1[j] = x1[j];
-          }
-          if (hh == 0 || ch + 1 < nch) fetch(c32 + 32);
-          uint32_t v[32];
-          tmem_ld32(taddr + ch * 64 + hh * 32, v);
-          tmem_ld_wait(v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t w0[4] = {y0[j].x, y0[j].y, y0[j].z, y0[j].w};
-            const uint32_t w1[4] = {y1[j].x, y1[j].y, y1[j].z, y1[j].w};
-            float dj[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (by_col && c32 + j * 8 < p.cols) {
-              const float4 lo = __ldg(reinterpret_cast<const float4*>(dv + c32 + j * 8));
-              const float4 hi = __ldg(reinterpret_cast<const float4*>(dv + c32 + j * 8 + 4));
-              dj[0] = lo.x, dj[1] = lo.y, dj[2] = lo.z, dj[3] = lo.w;
-              dj[4] = hi.x, dj[5] = hi.y, dj[6] = hi.z, dj[7] = hi.w;
-            }
-            uint32_t o0[4], o1[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float r[2];
-              const float2 in = unpack_f16x2(w0[e]);
-              const float2 inl = unpack_f16x2(w1[e]);
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const int col = c32 + j * 8 + 2 * e + t;
-                const float ac = __uint_as_float(v[j * 8 + 2 * e + t]);
-                const float i0 = t ? in.y : in.x;
-                const float d = dj[2 * e + t];
-                if (KIND == kNsGram) {
-                  r[t] = ac * (kNsScaleA / (kNsScaleX * kNsScaleX));
-                } else if (KIND == kNsSquare) {
-                  // true values: A_ij = i0 / S_A, (A^2)_ij = ac / S_A^2 + (d_i + d_j) A_ij
-                  float sq = fmaf(di + d, i0 * (1.f / kNsScaleA), ac * (1.f / (kNsScaleA * kNsScaleA)));
-                  float lin = i0 * (1.f / kNsScaleA);
-                  if (rt == ct && col == row) {
-                    sq = fmaf(d, d, sq);
-                    lin += d;
-                  }
-                  r[t] = fmaf(p.c, sq, p.b * lin) * kNsScaleB;
-                } else {
-                  const float x = i0 + (t ? inl.y : inl.x);
-                  r[t] = fmaf(p.a, x, fmaf(p.tall ? d : di, x, ac * (1.f / kNsScaleB)));
-                }
-                if (KIND != kNsUpdate && rt == ct && col == row && live)
-                  p.d_out[static_cast<size_t>(bz) * p.rows + row] =
-                      (r[t] - __half2float(__float2half_rn(r[t]))) *
-                      (KIND == kNsGram ? 1.f / kNsScaleA : 1.f / kNsScaleB);
-              }
-              if (KIND == kNsUpdate && p.last) {
-                o0[e] = pack_bf16x2(r[0] * (1.f / kNsScaleX), r[1] * (1.f / kNsScaleX));
-                o1[e] = 0;
-              } else {
-                o0[e] = pack_f16x2(r[0], r[1]);
-                const float2 h = unpack_f16x2(o0[e]);
-                o1[e] = KIND == kNsUpdate ? pack_f16x2(r[0] - h.x, r[1] - h.y) : 0u;
-              }
-            }
-            st_shared_v4(S0 + sw128_off(lane, hh * 4 + j), make_uint4(o0[0], o0[1], o0[2], o0[3]));
-            if (KIND == kNsUpdate && p.has_low)
-              st_shared_v4(S1 + sw128_off(lane, hh * 4 + j), make_uint4(o1[0], o1[1], o1[2], o1[3]));
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&p.out0, S0, cc, row0, bz);
-          if (KIND == kNsUpdate && p.has_low) tma_store_3d(&p.out1, S1, cc, row0, bz);
-          bulk_commit();
-        }
-        ++cnt;
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR)
-          mbar_arrive_cluster(tempty0 + acc * 8);
+    bool ok = true;
+    for (int ph = 0; ok && ph < phases; ++ph) {
+      const int kind = ph % 3, k = ph / 3;
+      const int nunits = p.geo[kind].whole + p.geo[kind].rest * p.geo[kind].splits;
+      // (also without a unit: an arrival must not come before the previous barrier)
+      if (ph > 0 && !__all_sync(0xffffffffu, mbar_wait(go, (ph - 1) & 1, w))) break;
+      if (lane == 0) fence_proxy_async_global();
+      for (int u = first; ok && u < nunits; u += step, ++it) {
+        const NsUnit n = ns_unit(p, kind, u);
+        const int acc = it & 1;
+        const uint32_t par = (it >> 1) & 1;
+        if (kind == kNsGram)
+          ok = ns_epilogue<kNsGram, PAIR>(p, n, k, acc, par, tfull, e, w);
+        else if (kind == kNsSquare)
+          ok = ns_epilogue<kNsSquare, PAIR>(p, n, k, acc, par, tfull, e, w);
         else
-          mbar_arrive(&tempty[acc]);
+          ok = ns_epilogue<kNsUpdate, PAIR>(p, n, k, acc, par, tfull, e, w);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(tempty0 + acc * 8);
+          else
+            mbar_arrive(&tempty[acc]);
+        }
+      }
+      if (!ok) break;
+      // this warp's results of the phase are in memory: arrive
+      if (lane == 0) {
+        bulk_wait_all<0>();
+        fence_proxy_async_global();
+      }
+      __threadfence();  // (every lane's own stores)
+      __syncwarp();
+      if (lane == 0 && ph + 1 < phases) {
+        // the CTA's last warp arrives for all of them
+        if (atomicAdd(warps_done, 1) == kNsEpiWarps * (ph + 1) - 1) {
+          __threadfence();
+          red_release_add(p.counters, 1);
+        }
       }
     }
     if (lane == 0) bulk_wait_all<0>();
@@ -525,15 +734,19 @@ __global__ void __launch_bounds__(kNsNormThreads) ns_sumsq_kernel(const float* _
   if (threadIdx.x == 0) part[static_cast<size_t>(blockIdx.y) * nblk + blockIdx.x] = s;
 }
 
-// X_0 = G / (|G|_F + eps), times the stored scale, as high and low fp16 parts.
+// X_0 = G / (|G|_F + eps), times the stored scale, as high and low fp16 parts
+// (and the counters of ns_kernel, which runs next, set to zero).
 // The factor goes on in two steps so that it may pass fp32's range (a G of
 // 1e-30 with eps 0).
 __global__ void __launch_bounds__(kNsNormThreads) ns_scale_kernel(const float* __restrict__ G, size_t n8, int nblk,
                                                                  const double* __restrict__ part, double eps,
-                                                                 __half* __restrict__ hi, __half* __restrict__ lo) {
+                                                                 __half* __restrict__ hi, __half* __restrict__ lo,
+                                                                 int* __restrict__ counters, int ncounters) {
   __shared__ double red[kNsNormThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < ncounters; i += kNsNormThreads) counters[i] = 0;
   double s = 0.0;
   for (int i = threadIdx.x; i < nblk; i += kNsNormThreads) s += part[static_cast<size_t>(blockIdx.y) * nblk + i];
   s = ns_block_sum(s, red);

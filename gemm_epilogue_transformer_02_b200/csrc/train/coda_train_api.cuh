@@ -105,13 +105,13 @@ inline int norm8_bwd_blocks(int64_t M, int64_t N) {
 
 constexpr int kNsMaxNormBlocks = 512;
 
+constexpr int kNsMaxCounters = 1 + 3 * kNsSplitCounters;
+
 struct NsPlan {
   int64_t batch, m, n, s;  // s: the smaller side
-  bool tall;
-  int block;     // tile of the symmetric results: 256 (CTA pairs) or 128
-  bool pair_up;  // the update runs on CTA pairs
+  bool tall, pair;         // pair: 256 x 256 tiles on CTA pairs, else 128 x 128
   int norm_blocks;
-  size_t hi[2], lo[2], A, B, dA, dB, part, bytes;
+  size_t hi[2], lo[2], A, B, dA, dB, sums, counters, part, bytes;
 };
 
 inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
@@ -121,99 +121,116 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
   p.n = n;
   p.tall = m > n;
   p.s = p.tall ? n : m;
-  p.block = p.s >= 1024 ? 256 : 128;
-  p.pair_up = p.block == 256;
+  p.pair = p.s >= 1024;
   const int64_t n8 = m * n / 8;
   p.norm_blocks = static_cast<int>(std::min<int64_t>(kNsMaxNormBlocks, (n8 + 2047) / 2048));
   size_t o = 0;
-  const size_t x = align256(static_cast<size_t>(batch) * m * n * 2);
-  const size_t sq = align256(static_cast<size_t>(batch) * p.s * p.s * 2);
-  const size_t dg = align256(static_cast<size_t>(batch) * p.s * 4);
+  const auto take = [&o](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
   for (int i = 0; i < 2; ++i) {
-    p.hi[i] = o;
-    p.lo[i] = o + x;
-    o += 2 * x;
+    p.hi[i] = take(static_cast<size_t>(batch) * m * n * 2);
+    p.lo[i] = take(static_cast<size_t>(batch) * m * n * 2);
   }
-  p.A = o;
-  p.B = o + sq;
-  p.dA = o + 2 * sq;
-  p.dB = p.dA + dg;
-  p.part = p.dB + dg;
-  p.bytes = p.part + align256(static_cast<size_t>(batch) * p.norm_blocks * 8);
+  p.A = take(static_cast<size_t>(batch) * p.s * p.s * 2);
+  p.B = take(static_cast<size_t>(batch) * p.s * p.s * 2);
+  p.dA = take(static_cast<size_t>(batch) * p.s * 4);
+  p.dB = take(static_cast<size_t>(batch) * p.s * 4);
+  p.sums = take(static_cast<size_t>(batch) * p.norm_blocks * 8);
+  p.counters = take(kNsMaxCounters * 4);
+  // at most one split unit per CTA (pair) of the grid
+  p.part = take(static_cast<size_t>(148) * 128 * (p.pair ? 256 : 128) * 4);
+  p.bytes = o;
   return p;
 }
 
-// [batch, rows, cols] of 2-byte elements, box box_rows x 64, 128-byte swizzle;
-// out-of-range elements read as zero and are not written.
+// [batch, rows, cols] of 2-byte elements, box box_rows x 64 with the 128-byte
+// swizzle, or box_rows x 32 with the 64-byte one; out-of-range elements read as
+// zero and are not written.
 bool tmap3d(CUtensorMap* m, const void* base, bool bf16, uint64_t cols, uint64_t rows, uint64_t batch,
-            uint32_t box_rows) {
+            uint32_t box_rows, uint32_t box_cols = 64) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[3] = {cols, rows, batch};
   cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
-  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
-// An operand with `rows` output rows (or columns) and K: stored [rows, K], [K, rows] or symmetric.
-bool ns_operand(NsOperand* o, const void* p, int major, uint64_t rows, uint64_t K, uint64_t batch) {
-  o->major = major;
-  bool ok = true;
-  if (major != kNsMN) ok = ok && tmap3d(&o->k, p, false, K, rows, batch, 128);
-  if (major != kNsK) ok = ok && tmap3d(&o->mn, p, false, rows, K, batch, 64);
-  return ok;
+// A GEMM's tiles over `slots` CTAs (or pairs).  Whole rounds of tiles are one
+// unit each.  A last round that fills at most half of the slots is split by
+// k-blocks, into two parts or, on pairs, four, if they fit and are at least
+// eight k-blocks long: the parts exchange accumulators through memory (about 4
+// us), which costs less than the k-blocks it saves only then.
+NsGeo ns_geo(int64_t batch, int64_t rows, int64_t cols, int64_t K, bool sym, int tile, int slots) {
+  NsGeo g;
+  g.rows = static_cast<int>(rows);
+  g.cols = static_cast<int>(cols);
+  g.nkb = static_cast<int>((K + 63) / 64);
+  g.n_rt = static_cast<int>((rows + tile - 1) / tile);
+  g.n_ct = static_cast<int>((cols + tile - 1) / tile);
+  g.tiles = sym ? g.n_rt * (g.n_rt + 1) / 2 : g.n_rt * g.n_ct;
+  const int all = static_cast<int>(batch) * g.tiles;
+  g.rest = all % slots;
+  g.whole = all - g.rest;
+  g.splits = 1;
+  while (g.rest > 0 && 2 * g.splits <= (tile == 256 ? 4 : 2) && 2 * g.splits * g.rest <= slots &&
+         g.nkb / (2 * g.splits) >= 8)
+    g.splits *= 2;
+  return g;
 }
 
-template <int KIND, bool PAIR>
-coda_status_t ns_launch(int dev, DevInfo* info, NsParams& p, cudaStream_t stream) {
+template <bool PAIR>
+coda_status_t ns_launch(int dev, DevInfo* info, NsParams& p, const NsPlan& pl, cudaStream_t stream) {
   static bool done[64];
-  static int clusters[64];
-  auto kern = ns_gemm_kernel<KIND, PAIR>;
+  static int slots[64];  // CTAs (or pairs) resident at once
+  auto kern = ns_kernel<PAIR>;
   constexpr int kTile = PAIR ? 256 : 128;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kNsThreads, 1, 1);
+  cfg.dynamicSmemBytes = kNsSmemBytes;
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (!done[dev]) {
       if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmemBytes) != cudaSuccess)
         return CODA_ERR_LAUNCH;
-      clusters[dev] = info->sms;
+      int n = info->sms;
       if (PAIR) {
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(2 * (info->sms / 2), 1, 1);
-        cfg.blockDim = dim3(kNsThreads, 1, 1);
-        cfg.dynamicSmemBytes = kNsSmemBytes;
-        cfg.attrs = attr;
+        cfg.attrs = attr + 1;
         cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
-          cudaGetLastError();
-          n = info->sms / 2;
-        }
-        clusters[dev] = n;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return CODA_ERR_LAUNCH;
       }
+      slots[dev] = std::min(n, PAIR ? 74 : 148);  // (the workspace has room for that many)
       done[dev] = true;
     }
   }
-  p.n_rt = (p.rows + kTile - 1) / kTile;
-  p.n_ct = (p.cols + kTile - 1) / kTile;
-  const int64_t tiles = KIND == kNsUpdate ? static_cast<int64_t>(p.n_rt) * p.n_ct
-                                          : static_cast<int64_t>(p.n_rt) * (p.n_rt + 1) / 2;
-  if (tiles * p.batch > kMaxInt) return CODA_ERR_SHAPE;
-  p.tiles = static_cast<int>(tiles);
+  const int64_t s = pl.s, l = pl.tall ? pl.m : pl.n;
+  p.geo[kNsGram] = ns_geo(pl.batch, s, s, l, true, kTile, slots[dev]);
+  p.geo[kNsSquare] = ns_geo(pl.batch, s, s, s, true, kTile, slots[dev]);
+  p.geo[kNsUpdate] = ns_geo(pl.batch, pl.m, pl.n, s, false, kTile, slots[dev]);
+  int n = 0;
+  for (const NsGeo& g : p.geo) n = std::max(n, g.whole > 0 ? slots[dev] : g.rest * g.splits);
   p.wait_ns = static_cast<uint64_t>(g_wait_ns);
-  const int units = p.tiles * p.batch;
-  const int n = units < clusters[dev] ? units : clusters[dev];
-  return launch_pdl(kern, dim3(static_cast<unsigned>(PAIR ? 2 * n : n)), kNsThreads, kNsSmemBytes, PAIR ? 2 : 0,
-                    stream, p);
+  cfg.gridDim = dim3(static_cast<unsigned>(PAIR ? 2 * n : n), 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -379,77 +396,49 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
   if (batch == 0) return CODA_OK;
   const NsPlan pl = ns_plan(batch, m, n);
   CODA_CHECK(ws && ws_bytes >= pl.bytes, CODA_ERR_WORKSPACE);
-  const int64_t rt = (m + 127) / 128, ct = (n + 127) / 128;
-  CODA_CHECK(batch * rt * ct <= kMaxInt, CODA_ERR_SHAPE);
+  CODA_CHECK(batch * ((m + 127) / 128) * ((n + 127) / 128) <= kMaxInt, CODA_ERR_SHAPE);
   int dev;
   DevInfo* info;
   coda_status_t st = current_device(&dev, &info);
   if (st != CODA_OK) return st;
   cudaStream_t stm = static_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(ws);
+  double* sums = reinterpret_cast<double*>(w + pl.sums);
+  NsParams p{};
   __half* hi[2] = {reinterpret_cast<__half*>(w + pl.hi[0]), reinterpret_cast<__half*>(w + pl.hi[1])};
   __half* lo[2] = {reinterpret_cast<__half*>(w + pl.lo[0]), reinterpret_cast<__half*>(w + pl.lo[1])};
   __half* A = reinterpret_cast<__half*>(w + pl.A);
   __half* B = reinterpret_cast<__half*>(w + pl.B);
-  float* dA = reinterpret_cast<float*>(w + pl.dA);
-  float* dB = reinterpret_cast<float*>(w + pl.dB);
-  double* part = reinterpret_cast<double*>(w + pl.part);
+  p.dA = reinterpret_cast<float*>(w + pl.dA);
+  p.dB = reinterpret_cast<float*>(w + pl.dB);
+  p.part = reinterpret_cast<float*>(w + pl.part);
+  p.counters = reinterpret_cast<int*>(w + pl.counters);
+  p.batch = static_cast<int>(batch);
+  p.steps = steps;
+  p.tall = pl.tall ? 1 : 0;
+  p.a = a;
+  p.b = b;
+  p.c = c;
+  const int64_t s = pl.s;
+  bool ok = true;
+  for (int i = 0; i < 2; ++i)
+    ok = ok && tmap3d(&p.Xk[i], hi[i], false, n, m, batch, 128) && tmap3d(&p.Xmn[i], hi[i], false, n, m, batch, 64) &&
+         tmap3d(&p.Hbox[i], hi[i], false, n, m, batch, 32, 32) && tmap3d(&p.Lbox[i], lo[i], false, n, m, batch, 32, 32);
+  ok = ok && tmap3d(&p.Ak, A, false, s, s, batch, 128) && tmap3d(&p.Amn, A, false, s, s, batch, 64) &&
+       tmap3d(&p.Abox, A, false, s, s, batch, 32, 32) && tmap3d(&p.Bk, B, false, s, s, batch, 128) &&
+       tmap3d(&p.Bmn, B, false, s, s, batch, 64) && tmap3d(&p.Bbox, B, false, s, s, batch, 32, 32) &&
+       tmap3d(&p.Obox, out, true, n, m, batch, 32, 32);
+  if (!ok) return CODA_ERR_INTERNAL;
   const size_t n8 = static_cast<size_t>(m) * n / 8;
   st = launch_pdl(ns_sumsq_kernel, dim3(static_cast<unsigned>(pl.norm_blocks), static_cast<unsigned>(batch)),
-                  kNsNormThreads, 0, 0, stm, G, n8, pl.norm_blocks, part);
+                  kNsNormThreads, 0, 0, stm, G, n8, pl.norm_blocks, sums);
   if (st != CODA_OK) return st;
   st = launch_pdl(ns_scale_kernel, dim3(static_cast<unsigned>(pl.norm_blocks), static_cast<unsigned>(batch)),
-                  kNsNormThreads, 0, 0, stm, G, n8, pl.norm_blocks, static_cast<const double*>(part),
-                  static_cast<double>(eps), hi[0], steps > 1 ? lo[0] : static_cast<__half*>(nullptr));
+                  kNsNormThreads, 0, 0, stm, G, n8, pl.norm_blocks, static_cast<const double*>(sums),
+                  static_cast<double>(eps), hi[0], steps > 1 ? lo[0] : static_cast<__half*>(nullptr), p.counters,
+                  kNsMaxCounters);
   if (st != CODA_OK) return st;
-  const int64_t s = pl.s, l = pl.tall ? m : n;  // smaller and larger side
-  NsParams gr{}, sq{}, up{};
-  gr.batch = sq.batch = up.batch = static_cast<int>(batch);
-  gr.sym_block = sq.sym_block = up.sym_block = pl.block;
-  gr.a = sq.a = up.a = a;
-  gr.b = sq.b = up.b = b;
-  gr.c = sq.c = up.c = c;
-  gr.rows = gr.cols = sq.rows = sq.cols = sq.K = static_cast<int>(s);
-  gr.K = static_cast<int>(l);
-  gr.d_out = dA;
-  sq.in0 = A;
-  sq.d_in = dA;
-  sq.d_out = dB;
-  up.rows = static_cast<int>(m);
-  up.cols = static_cast<int>(n);
-  up.K = static_cast<int>(s);
-  up.d_in = dB;
-  up.tall = pl.tall ? 1 : 0;
-  bool ok = ns_operand(&sq.P, A, kNsSym, s, s, batch) && tmap3d(&gr.out0, A, false, s, s, batch, 32) &&
-            tmap3d(&sq.out0, B, false, s, s, batch, 32);
-  sq.Q = sq.P;
-  for (int k = 0; ok && k < steps; ++k) {
-    const __half* x = hi[k & 1];
-    const bool last = k + 1 == steps;
-    // X [m, n]: for X X^T its rows are the operands' rows; for X^T X its columns
-    ok = ns_operand(&gr.P, x, pl.tall ? kNsMN : kNsK, s, l, batch);
-    gr.Q = gr.P;
-    if (pl.tall)
-      ok = ok && ns_operand(&up.P, x, kNsK, m, s, batch) && ns_operand(&up.Q, B, kNsSym, s, s, batch);
-    else
-      ok = ok && ns_operand(&up.P, B, kNsSym, s, s, batch) && ns_operand(&up.Q, x, kNsMN, n, s, batch);
-    up.in0 = x;
-    up.in1 = last ? nullptr : lo[k & 1];
-    up.last = last ? 1 : 0;
-    up.has_low = k + 2 < steps ? 1 : 0;
-    ok = ok && (last ? tmap3d(&up.out0, out, true, n, m, batch, 32)
-                     : tmap3d(&up.out0, hi[(k + 1) & 1], false, n, m, batch, 32));
-    ok = ok && (!up.has_low || tmap3d(&up.out1, lo[(k + 1) & 1], false, n, m, batch, 32));
-    if (!ok) return CODA_ERR_INTERNAL;
-    st = pl.block == 256 ? ns_launch<kNsGram, true>(dev, info, gr, stm) : ns_launch<kNsGram, false>(dev, info, gr, stm);
-    if (st != CODA_OK) return st;
-    st = pl.block == 256 ? ns_launch<kNsSquare, true>(dev, info, sq, stm)
-                         : ns_launch<kNsSquare, false>(dev, info, sq, stm);
-    if (st != CODA_OK) return st;
-    st = pl.pair_up ? ns_launch<kNsUpdate, true>(dev, info, up, stm) : ns_launch<kNsUpdate, false>(dev, info, up, stm);
-    if (st != CODA_OK) return st;
-  }
-  return ok ? CODA_OK : CODA_ERR_INTERNAL;
+  return pl.pair ? ns_launch<true>(dev, info, p, pl, stm) : ns_launch<false>(dev, info, p, pl, stm);
 }
 
 }  // extern "C"
