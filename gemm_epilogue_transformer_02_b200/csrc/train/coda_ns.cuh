@@ -27,8 +27,9 @@
 // roundings off the result where they would grow:
 //   - near the end A and B are close to multiples of the identity, and most of
 //     their norm is on the diagonal.  What fp16 drops there is kept in fp32
-//     (dA, dB: one value per row) and applied by the epilogues:
-//     (A + D)^2 = A^2 + D A + A D + D^2, and (B + E) X = B X + E X;
+//     (dA, dB: one value per row) and applied by the epilogues: 2 D A + D^2 on
+//     the diagonal of the square (off it D A is as small as the rounding of A's
+//     other entries), and (B + E) X = B X + E X;
 //   - a small singular value grows by up to `a` in every step, and so does what
 //     rounding X put there.  X is therefore kept as a high and a low fp16 part;
 //     the GEMMs read the high part and the term a X both.  The last step drops
@@ -131,6 +132,64 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+// Two fp32 values in a 64-bit register pair: one instruction for both.
+__device__ __forceinline__ uint64_t f2_bits(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_set(float x, float y) { return f2_bits(__float_as_uint(x), __float_as_uint(y)); }
+__device__ __forceinline__ float2 f2_get(uint64_t v) {
+  uint32_t x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
+  return make_float2(__uint_as_float(x), __uint_as_float(y));
+}
+__device__ __forceinline__ uint64_t f2_half(uint32_t h) {  // two fp16 values
+  const float2 f = unpack_f16x2(h);
+  return f2_set(f.x, f.y);
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) { return f2_fma(b, f2_set(-1.f, -1.f), a); }
+
+// Wait (bounded) until *addr >= target, polling without a pause: few threads
+// wait, and each poll takes a trip to L2.
+__device__ __noinline__ bool ns_count_wait(const int* addr, int target, const WaitCtx& w) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (ld_acquire(addr) >= target) return true;
+    if ((i & 63u) == 0) {
+      if (*w.abort_flag) return false;
+      if (globaltimer_ns() - t0 > w.limit_ns) {
+        *w.abort_flag = 1;
+        atomicCAS(&g_coda_status, 0, kDevTimeout);
+        return false;
+      }
+    }
+  }
+}
+
+// Adds to a counter in shared memory and returns its old value; orders this
+// thread's accesses with those of the CTA's other threads that add to it.
+__device__ __forceinline__ int add_acq_rel_cta(int* addr, int v) {
+  int old;
+  asm volatile("atom.acq_rel.cta.shared::cta.add.s32 %0, [%1], %2;" : "=r"(old) : "r"(smem_u32(addr)), "r"(v) : "memory");
+  return old;
+}
+
 // A unit of work: a tile (matrix, row tile, column tile) and its k-blocks.
 struct NsUnit {
   int bz, rt, ct;
@@ -209,7 +268,7 @@ __device__ __forceinline__ uint32_t sw64_off(int row, int chunk) {
   return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
 }
 
-constexpr int kNsSplitCounters = 74 * 16;  // of one GEMM: split tiles (at most half of the slots) x warps
+constexpr int kNsSplitCounters = 37 * 16;  // of one GEMM: split tiles (at most half of the slots) x warps
 
 // What an epilogue warp keeps.
 struct NsEpi {
@@ -232,17 +291,17 @@ __device__ __forceinline__ void ns_add4(uint32_t (&v)[32], int j, const float4& 
 
 // One unit's epilogue for one warp: 32 rows x half of the tile's columns, in
 // blocks of 32 columns (a thread has one row).  A block's inputs come by TMA
-// into a staging buffer, one block ahead; the thread replaces its row by the
-// results, which leave by TMA from the same buffer.  (Direct loads of a row per
-// thread touch 32 lines an instruction and bound the update at 20 us a tile.)
-// The loop over blocks is not unrolled: three epilogues alternate in this
-// kernel, and straight-line code that runs once per GEMM is bound by
-// instruction fetches.  Returns false if a wait gave up.
+// into a staging buffer, one block ahead (the first one's during the main
+// loop); the thread replaces its row by the results, which leave by TMA from the
+// same buffer.  (Direct loads of a row per thread touch 32 lines an instruction
+// and bound the update at 20 us a tile.)  Sixteen warps with a quarter of the
+// columns each, or tensor-memory loads of 8 columns in a small loop, were
+// slower.  Returns false if a wait gave up.
 template <int KIND, bool PAIR>
 __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, int k, int acc, uint32_t parity,
                                             uint64_t* tfull, NsEpi& e, const WaitCtx& w) {
   constexpr int kTile = PAIR ? 256 : 128;
-  constexpr int kHalf = kTile / 2;    // columns of this warp
+  constexpr int kHalf = kTile / 2;  // columns of this warp
   constexpr int kBlks = kHalf / 32;
   const NsGeo& g = p.geo[KIND];
   const bool last = k + 1 == p.steps;
@@ -255,11 +314,11 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
   const int row = row0 + lane;
   const int col0 = n.ct * kTile + e.half * kHalf;
   const bool live = row < g.rows;
-  // dA (square: of the row and of the column), dB (update: of the row of B X, of the column of X B)
-  const bool by_col = KIND == kNsSquare || (KIND == kNsUpdate && p.tall);
+  // dA of the row (square); dB of the row of B X, of the column of X B (update).
+  // Written by other CTAs of this launch: read through L2.
+  const bool by_col = KIND == kNsUpdate && p.tall;
   const float* dv = (KIND == kNsSquare ? p.dA : p.dB) + static_cast<size_t>(n.bz) * (by_col ? g.cols : g.rows);
-  float di = 0.f;
-  if (KIND == kNsSquare || (KIND == kNsUpdate && !by_col)) di = live ? __ldcg(dv + row) : 0.f;
+  const float di = KIND != kNsGram && !by_col && live ? __ldcg(dv + row) : 0.f;
   int nblk = (g.cols - col0 + 31) / 32;
   if (nblk > kBlks) nblk = kBlks;
   if (row0 >= g.rows || nblk < 0) nblk = 0;  // (uniform over the warp)
@@ -269,7 +328,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
     b0 = n.part * (kBlks / g.splits);
     b1 = min(nblk, b0 + kBlks / g.splits);
   }
-  float dc = 0.f;  // d of the block's column number `lane`
+  float dc = 0.f;  // a + d of the block's column number `lane`
   auto fetch = [&](int b, uint32_t cnt) {
     if (KIND == kNsGram) return;
     const int c = col0 + b * 32;
@@ -280,7 +339,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
       tma_load_3d(d, in0, &e.bars[cnt & 1], c, row0, n.bz);
       if (in_low) tma_load_3d(d + kNsBoxBytes, in1, &e.bars[cnt & 1], c, row0, n.bz);
     }
-    if (by_col) dc = c + lane < g.cols ? __ldcg(dv + c + lane) : 0.f;
+    if (by_col) dc = p.a + (c + lane < g.cols ? __ldcg(dv + c + lane) : 0.f);
   };
   if (b0 < b1) fetch(b0, e.cnt);
   // Warp-uniform outcomes: tcgen05.ld below is a warp-collective instruction.
@@ -289,9 +348,9 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
   const uint32_t taddr = e.taddr + acc * kTile + e.half * kHalf;
   // A split tile: each part hands the others' blocks of its accumulator over
   // through memory, waits for theirs and adds up the parts of its own blocks in
-  // an order that does not depend on whose they are.  The parts run at the same time (they are the last units of
-  // their CTAs in this GEMM).  A lane's float4 lie 512 bytes apart, so a warp's
-  // access is contiguous.
+  // an order that does not depend on whose they are.  The parts run at the same
+  // time (they are the last units of their CTAs in this GEMM).  A lane's float4
+  // lie 512 bytes apart, so a warp's access is contiguous.
   constexpr size_t kPart = static_cast<size_t>(PAIR ? 16 : 8) * 32 * kHalf / 4;  // float4 of a tile's part
   float4* part = nullptr;
   if (n.part >= 0 && nblk > 0) {
@@ -310,24 +369,21 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
                make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]), __uint_as_float(v[4 * j + 2]),
                            __uint_as_float(v[4 * j + 3])));
     }
-    __threadfence();
     __syncwarp();
     int ok = 1;
     if (lane == 0) {
       int* c = p.counters + 1 + KIND * kNsSplitCounters + n.split * (PAIR ? 16 : 8) + region;
       red_release_add(c, 1);
-      if (b0 < b1) ok = counter_wait(c, g.splits * (k + 1), w) ? 1 : 0;
-      __threadfence();
+      if (b0 < b1) ok = ns_count_wait(c, g.splits * (k + 1), w) ? 1 : 0;
     }
+    __syncwarp();
     if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
   }
-  const int dcol = KIND != kNsUpdate && n.rt == n.ct ? row : -1;  // this row's diagonal column, if the tile has it
-  float dval = 0.f;                                               // the value there
   // the accumulator's share: gram S_A / S_X^2, square c S_B / S_A^2, update 1 / S_B
   const float sc = KIND == kNsGram ? kNsScaleA / (kNsScaleX * kNsScaleX)
                                    : (KIND == kNsSquare ? p.c * (kNsScaleB / (kNsScaleA * kNsScaleA)) : 1.f / kNsScaleB);
-  // on the diagonal the square has b d + c d^2 more: (A + D)^2 = A^2 + D A + A D + D^2
-  const float corr = KIND == kNsSquare ? di * fmaf(p.c, di, p.b) * kNsScaleB : 0.f;
+  // the input's: square b S_B / S_A, update a + d of the row
+  const float si = KIND == kNsSquare ? p.b * (kNsScaleB / kNsScaleA) : p.a + di;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b, ++e.cnt) {
     const int c32 = col0 + b * 32;
@@ -342,6 +398,12 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
       if (b + 1 < b1) fetch(b + 1, e.cnt + 1);
       if (!__all_sync(0xffffffffu, mbar_wait(&e.bars[buf], (e.loads >> buf) & 1, w))) return false;
       e.loads ^= 1u << buf;
+    }
+    uint4 x0[4], x1[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (KIND != kNsGram) x0[j] = ld_shared_v4(S0 + sw64_off(lane, j));
+      if (in_low) x1[j] = ld_shared_v4(S1 + sw64_off(lane, j));
     }
     uint32_t v[32];
     tmem_ld32(taddr + b * 32, v);
@@ -366,48 +428,80 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
           ns_add4(v, j, make_float4(o[j].x + q[j].x, o[j].y + q[j].y, o[j].z + q[j].z, o[j].w + q[j].w));
       }
     }
-    const bool bf_out = KIND == kNsUpdate && last;
+    uint64_t r[16];  // the results, two to a register pair
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t off = sw64_off(lane, j);
-      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = make_uint4(0, 0, 0, 0);
-      if (KIND != kNsGram) x0 = ld_shared_v4(S0 + off);
-      if (in_low) x1 = ld_shared_v4(S1 + off);
-      const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
-      uint32_t o0[4], o1[4];
+    for (int i = 0; i < 16; ++i) r[i] = f2_mul(f2_bits(v[2 * i], v[2 * i + 1]), f2_set(sc, sc));
+    if (KIND != kNsGram) {
+      uint64_t in[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float r[2];
-        const float2 h = unpack_f16x2(w0[i]);
-        const float2 l = unpack_f16x2(w1[i]);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w0[4] = {x0[j].x, x0[j].y, x0[j].z, x0[j].w};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int at = j * 8 + 2 * i + u;
-          const float ac = __uint_as_float(v[at]);
-          const float f = u ? h.y : h.x;
-          const float d = by_col ? __shfl_sync(0xffffffffu, dcb, at) : 0.f;
-          if (KIND == kNsGram)
-            r[u] = ac * sc;
-          else if (KIND == kNsSquare)  // b A + c (d_i + d_j) A (stored with S_A, wanted with S_B) + c acc
-            r[u] = fmaf(ac, sc, f * fmaf(p.c, di + d, p.b) * (kNsScaleB / kNsScaleA));
-          else  // (a + d) X + acc
-            r[u] = fmaf(ac, sc, (p.a + (di + d)) * (f + (u ? l.y : l.x)));
-          if (KIND != kNsUpdate && c32 + at == dcol) {
-            r[u] += corr;
-            dval = r[u];
-          }
-        }
-        if (bf_out) {
-          o0[i] = pack_bf16x2(r[0] * (1.f / kNsScaleX), r[1] * (1.f / kNsScaleX));
-          o1[i] = 0;
-        } else {
-          o0[i] = pack_f16x2(r[0], r[1]);
-          const float2 hr = unpack_f16x2(o0[i]);
-          o1[i] = KIND == kNsUpdate ? pack_f16x2(r[0] - hr.x, r[1] - hr.y) : 0u;
+        for (int i = 0; i < 4; ++i) in[4 * j + i] = f2_half(w0[i]);
+      }
+      if (in_low) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w1[4] = {x1[j].x, x1[j].y, x1[j].z, x1[j].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) in[4 * j + i] = f2_add(in[4 * j + i], f2_half(w1[i]));
         }
       }
-      st_shared_v4(S0 + off, make_uint4(o0[0], o0[1], o0[2], o0[3]));
-      if (has_low) st_shared_v4(S1 + off, make_uint4(o1[0], o1[1], o1[2], o1[3]));
+      if (by_col) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          r[i] = f2_fma(in[i], f2_set(__shfl_sync(0xffffffffu, dcb, 2 * i), __shfl_sync(0xffffffffu, dcb, 2 * i + 1)),
+                        r[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = f2_fma(in[i], f2_set(si, si), r[i]);
+      }
+    }
+    if (KIND != kNsUpdate && c32 == row0) {
+      // the block of this row's diagonal entry, column `lane`
+      float corr = 0.f, dval = 0.f;
+      if (KIND == kNsSquare) {  // b d + c (2 d A + d^2)
+        const __half f = *reinterpret_cast<const __half*>(S0 + sw64_off(lane, lane >> 3) + (lane & 7) * 2);
+        corr = di * fmaf(p.c, fmaf(2.f / kNsScaleA, __half2float(f), di), p.b) * kNsScaleB;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float2 x = f2_get(r[i]);
+        x.x += lane == 2 * i ? corr : 0.f;
+        x.y += lane == 2 * i + 1 ? corr : 0.f;
+        dval = lane == 2 * i ? x.x : (lane == 2 * i + 1 ? x.y : dval);
+        r[i] = f2_set(x.x, x.y);
+      }
+      if (live)
+        (KIND == kNsGram ? p.dA : p.dB)[static_cast<size_t>(n.bz) * g.rows + row] =
+            (dval - __half2float(__float2half_rn(dval))) * (KIND == kNsGram ? 1.f / kNsScaleA : 1.f / kNsScaleB);
+    }
+    uint32_t o[16];
+    if (KIND == kNsUpdate && last) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 x = f2_get(f2_mul(r[i], f2_set(1.f / kNsScaleX, 1.f / kNsScaleX)));
+        o[i] = pack_bf16x2(x.x, x.y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 x = f2_get(r[i]);
+        o[i] = pack_f16x2(x.x, x.y);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      st_shared_v4(S0 + sw64_off(lane, j), make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+    if (has_low) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 x = f2_get(f2_sub(r[i], f2_half(o[i])));
+        o[i] = pack_f16x2(x.x, x.y);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        st_shared_v4(S1 + sw64_off(lane, j), make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
     }
     fence_async_smem();
     __syncwarp();
@@ -419,9 +513,6 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
       bulk_commit();
     }
   }
-  if (KIND != kNsUpdate && live && dcol >= col0 + b0 * 32 && dcol < col0 + b1 * 32)
-    (KIND == kNsGram ? p.dA : p.dB)[static_cast<size_t>(n.bz) * g.rows + row] =
-        (dval - __half2float(__float2half_rn(dval))) * (KIND == kNsGram ? 1.f / kNsScaleA : 1.f / kNsScaleB);
   return true;
 }
 
@@ -505,7 +596,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         ns_operands(p, kind, (ph / 3) & 1, op[0], op[1]);
         const int nunits = p.geo[kind].whole + p.geo[kind].rest * p.geo[kind].splits;
         if (ph > 0) {
-          if (!counter_wait(p.counters, arrivals * ph, w)) break;
+          if (!ns_count_wait(p.counters, arrivals * ph, w)) break;
           fence_proxy_async_global();  // the loads below see what other CTAs' copies wrote
           mbar_arrive(go);
         }
@@ -672,15 +763,11 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         bulk_wait_all<0>();
         fence_proxy_async_global();
       }
-      __threadfence();  // (every lane's own stores)
       __syncwarp();
-      if (lane == 0 && ph + 1 < phases) {
-        // the CTA's last warp arrives for all of them
-        if (atomicAdd(warps_done, 1) == kNsEpiWarps * (ph + 1) - 1) {
-          __threadfence();
-          red_release_add(p.counters, 1);
-        }
-      }
+      // the CTA's last warp arrives for all of them: its release covers what the
+      // others' lanes wrote before the warp barrier and their arrivals here
+      if (lane == 0 && ph + 1 < phases && add_acq_rel_cta(warps_done, 1) == kNsEpiWarps * (ph + 1) - 1)
+        red_release_add(p.counters, 1);
     }
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
