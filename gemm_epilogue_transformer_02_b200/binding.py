@@ -813,30 +813,52 @@ def block_backward(dOut, x, W1, W2, gamma, fwd):
 # ------------------------------------------------ around the GEMM chain
 #
 # These calls run on the device of their tensors (which must all be on one),
-# on that device's current stream.
+# on that device's current stream.  Their kernels take a few microseconds on
+# small inputs, so the checks are kept short on the way to the library: one
+# combined test per tensor, and the errors' wording only where it fails.
 
 
-def _on_one_device(**tensors):
-    """A guard for the device that all of the given tensors are on."""
-    devs = {t.device for t in tensors.values() if t is not None}
-    if len(devs) != 1:
-        raise ValueError("tensors on different devices: " + ", ".join(
-            f"{k} on {t.device}" for k, t in tensors.items() if t is not None))
-    return torch.cuda.device(devs.pop())
-
-
-def _workspace(ws, nbytes: int, like):
-    """The caller's workspace (a byte tensor; the library checks its size), or a new one."""
-    if ws is None:
-        return _empty((max(nbytes, 16),), U8, like)
-    return _need(ws, U8, "ws")
+def _ok(t, dtype, name, shape):
+    """_need with a shape, in one test where all is well."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_cuda
+            or not t.is_contiguous()):
+        _need(t, dtype, name, shape)
+    return t
 
 
 def _matrix(t, dtype, name):
     _need(t, dtype, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
-    return tuple(t.shape)
+    return t.shape
+
+
+def _out(t, dtype, name, shape, like):
+    """An output: the caller's, or a new one."""
+    return like.new_empty(shape, dtype=dtype) if t is None else _ok(t, dtype, name, shape)
+
+
+def _workspace(ws, nbytes: int, like):
+    """The caller's workspace (a byte tensor; the library checks its size), or a new one."""
+    return like.new_empty(nbytes if nbytes > 16 else 16, dtype=U8) if ws is None else _need(ws, U8, "ws")
+
+
+def _launch(name: str, tensors, *args):
+    """Calls the library on the device that all of the tensors are on."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: tensors on different devices: "
+                             + ", ".join(str(t.device) for t in tensors if t is not None))
+    if dev == torch._C._cuda_getDevice():
+        _call(name, *args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            _call(name, *args, torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def embed(tokens, E, scale: float = 1.0, gamma=None, *, h=True, partial=True, h_out=None, hg_out=None,
@@ -848,22 +870,16 @@ def embed(tokens, E, scale: float = 1.0, gamma=None, *, h=True, partial=True, h_
     V, D = _matrix(E, BF16, "E")
     _need(tokens, torch.int64, "tokens")
     M = tokens.numel()
-    _need(tokens, torch.int64, "tokens", (M,))
+    _ok(tokens, torch.int64, "tokens", (M,))
     if gamma is not None:
-        _need(gamma, BF16, "gamma", (D,))
+        _ok(gamma, BF16, "gamma", (D,))
+        hg_out = _out(hg_out, BF16, "hg_out", (M, D), E)
     elif hg_out is not None:
         raise ValueError("hg_out needs gamma")
-    h_out = (_empty((M, D), BF16, E) if h_out is None else _need(h_out, BF16, "h_out", (M, D))) if h else None
-    if gamma is not None:
-        hg_out = _empty((M, D), BF16, E) if hg_out is None else _need(hg_out, BF16, "hg_out", (M, D))
-    T = partial_cols(D)
-    if partial:
-        partial_out = _empty((T, M), F32, E) if partial_out is None else _need(partial_out, F32, "partial_out", (T, M))
-    else:
-        partial_out = None
-    with _on_one_device(tokens=tokens, E=E, gamma=gamma, h_out=h_out, hg_out=hg_out, partial_out=partial_out):
-        _call("coda_embed", _ptr(tokens), _ptr(E), float(scale), _ptr(gamma), _ptr(h_out), _ptr(hg_out),
-              _ptr(partial_out), M, D, V, _stream())
+    h_out = _out(h_out, BF16, "h_out", (M, D), E) if h else None
+    partial_out = _out(partial_out, F32, "partial_out", (-(-D // 128), M), E) if partial else None
+    _launch("coda_embed", (E, tokens, gamma, h_out, hg_out, partial_out), tokens.data_ptr(), E.data_ptr(), scale,
+            _addr(gamma), _addr(h_out), _addr(hg_out), _addr(partial_out), M, D, V)
     return h_out, hg_out, partial_out
 
 
@@ -872,38 +888,30 @@ def embed_bwd(tokens, dh, V: int, scale: float = 1.0, dE_out=None, accumulate: b
     (repeatable bits).  accumulate adds to dE_out and touches only the rows of
     tokens that occur."""
     M, D = _matrix(dh, BF16, "dh")
-    _need(tokens, torch.int64, "tokens", (M,))
+    _ok(tokens, torch.int64, "tokens", (M,))
     if accumulate and dE_out is None:
         raise ValueError("accumulate needs dE_out")
-    dE_out = _empty((int(V), D), F32, dh) if dE_out is None else _need(dE_out, F32, "dE_out", (int(V), D))
-    ws = _workspace(ws, int(load_library().coda_embed_bwd_workspace_size(M, D)), dh)
-    with _on_one_device(tokens=tokens, dh=dh, dE_out=dE_out, ws=ws):
-        _call("coda_embed_bwd", _ptr(tokens), _ptr(dh), float(scale), _ptr(dE_out), 1 if accumulate else 0, _ptr(ws),
-              ws.numel(), M, D, int(V), _stream())
+    dE_out = _out(dE_out, F32, "dE_out", (V, D), dh)
+    ws = _workspace(ws, load_library().coda_embed_bwd_workspace_size(M, D), dh)
+    _launch("coda_embed_bwd", (dh, tokens, dE_out, ws), tokens.data_ptr(), dh.data_ptr(), scale, dE_out.data_ptr(),
+            1 if accumulate else 0, ws.data_ptr(), ws.numel(), M, D, V)
     return dE_out
-
-
-def _norm_inputs(x, res, gamma, h, h_out, r_out):
-    M, N = _matrix(x, BF16, "x")
-    if res is not None:
-        _need(res, BF16, "res", (M, N))
-    _need(gamma, BF16, "gamma", (N,))
-    h_out = (_empty((M, N), BF16, x) if h_out is None else _need(h_out, BF16, "h_out", (M, N))) if h else None
-    r_out = _empty((M,), F32, x) if r_out is None else _need(r_out, F32, "r_out", (M,))
-    return M, N, h_out, r_out
 
 
 def add_rmsnorm_mx(x, res, gamma, eps: float, *, h=True, h_out=None, yq_out=None, ysf_out=None, r_out=None):
     """h = x + res (res may be None), y = gamma * h / sqrt(mean(h^2) + eps) in
     MXFP8 for gemm_rowscale_partial_mx.  Returns (h bf16 or None, codes uint8
     [M, N], scales uint8 in the A layout, r [M])."""
-    M, N, h_out, r_out = _norm_inputs(x, res, gamma, h, h_out, r_out)
-    yq_out = _empty((M, N), U8, x) if yq_out is None else _need(yq_out, U8, "yq_out", (M, N))
-    nsf = mx_sf_bytes(M, N, MX_A) if M else 0
-    ysf_out = _empty((nsf,), U8, x) if ysf_out is None else _need(ysf_out, U8, "ysf_out", (nsf,))
-    with _on_one_device(x=x, res=res, gamma=gamma, h_out=h_out, yq_out=yq_out, ysf_out=ysf_out, r_out=r_out):
-        _call("coda_add_rmsnorm_mx", _ptr(x), _ptr(res), _ptr(gamma), float(eps), _ptr(h_out), _ptr(yq_out),
-              _ptr(ysf_out), _ptr(r_out), M, N, _stream())
+    M, N = _matrix(x, BF16, "x")
+    if res is not None:
+        _ok(res, BF16, "res", (M, N))
+    _ok(gamma, BF16, "gamma", (N,))
+    h_out = _out(h_out, BF16, "h_out", (M, N), x) if h else None
+    yq_out = _out(yq_out, U8, "yq_out", (M, N), x)
+    ysf_out = _out(ysf_out, U8, "ysf_out", (mx_sf_bytes(M, N, MX_A) if M else 0,), x)
+    r_out = _out(r_out, F32, "r_out", (M,), x)
+    _launch("coda_add_rmsnorm_mx", (x, res, gamma, h_out, yq_out, ysf_out, r_out), x.data_ptr(), _addr(res),
+            gamma.data_ptr(), eps, _addr(h_out), yq_out.data_ptr(), ysf_out.data_ptr(), r_out.data_ptr(), M, N)
     return h_out, yq_out, ysf_out, r_out
 
 
@@ -911,14 +919,18 @@ def add_rmsnorm_fp8(x, res, gamma, eps: float, s_y, *, h=True, h_out=None, y8_ou
     """h = x + res (res may be None), y8 = e4m3(gamma * h * r / s_y) for
     gemm_fp8, amax = max |y|.  Returns (h bf16 or None, y8 uint8 [M, N], amax
     [1], r [M])."""
-    M, N, h_out, r_out = _norm_inputs(x, res, gamma, h, h_out, r_out)
-    _need(s_y, F32, "s_y", (1,))
-    y8_out = _empty((M, N), U8, x) if y8_out is None else _need(y8_out, U8, "y8_out", (M, N))
-    amax_out = _empty((1,), F32, x) if amax_out is None else _need(amax_out, F32, "amax_out", (1,))
-    with _on_one_device(x=x, res=res, gamma=gamma, s_y=s_y, h_out=h_out, y8_out=y8_out, amax_out=amax_out,
-                        r_out=r_out):
-        _call("coda_add_rmsnorm_fp8", _ptr(x), _ptr(res), _ptr(gamma), float(eps), _ptr(s_y), _ptr(h_out),
-              _ptr(y8_out), _ptr(amax_out), _ptr(r_out), M, N, _stream())
+    M, N = _matrix(x, BF16, "x")
+    if res is not None:
+        _ok(res, BF16, "res", (M, N))
+    _ok(gamma, BF16, "gamma", (N,))
+    _ok(s_y, F32, "s_y", (1,))
+    h_out = _out(h_out, BF16, "h_out", (M, N), x) if h else None
+    y8_out = _out(y8_out, U8, "y8_out", (M, N), x)
+    amax_out = _out(amax_out, F32, "amax_out", (1,), x)
+    r_out = _out(r_out, F32, "r_out", (M,), x)
+    _launch("coda_add_rmsnorm_fp8", (x, res, gamma, s_y, h_out, y8_out, amax_out, r_out), x.data_ptr(), _addr(res),
+            gamma.data_ptr(), eps, s_y.data_ptr(), _addr(h_out), y8_out.data_ptr(), amax_out.data_ptr(),
+            r_out.data_ptr(), M, N)
     return h_out, y8_out, amax_out, r_out
 
 
@@ -927,17 +939,17 @@ def add_rmsnorm_bwd(dy, h, r, gamma, d_h=None, dx_out=None, dgamma_out=None, ws=
     (of x and of res; d_h, the residual stream's gradient, is added) bf16 and
     dgamma fp32.  Returns (dx, dgamma)."""
     M, N = _matrix(dy, BF16, "dy")
-    _need(h, BF16, "h", (M, N))
-    _need(r, F32, "r", (M,))
-    _need(gamma, BF16, "gamma", (N,))
+    _ok(h, BF16, "h", (M, N))
+    _ok(r, F32, "r", (M,))
+    _ok(gamma, BF16, "gamma", (N,))
     if d_h is not None:
-        _need(d_h, BF16, "d_h", (M, N))
-    dx_out = _empty((M, N), BF16, dy) if dx_out is None else _need(dx_out, BF16, "dx_out", (M, N))
-    dgamma_out = _empty((N,), F32, dy) if dgamma_out is None else _need(dgamma_out, F32, "dgamma_out", (N,))
-    ws = _workspace(ws, int(load_library().coda_add_rmsnorm_bwd_workspace_size(M, N)), dy)
-    with _on_one_device(dy=dy, h=h, r=r, gamma=gamma, d_h=d_h, dx_out=dx_out, dgamma_out=dgamma_out, ws=ws):
-        _call("coda_add_rmsnorm_bwd", _ptr(dy), _ptr(h), _ptr(r), _ptr(gamma), _ptr(d_h), _ptr(dx_out),
-              _ptr(dgamma_out), _ptr(ws), ws.numel(), M, N, _stream())
+        _ok(d_h, BF16, "d_h", (M, N))
+    dx_out = _out(dx_out, BF16, "dx_out", (M, N), dy)
+    dgamma_out = _out(dgamma_out, F32, "dgamma_out", (N,), dy)
+    ws = _workspace(ws, load_library().coda_add_rmsnorm_bwd_workspace_size(M, N), dy)
+    _launch("coda_add_rmsnorm_bwd", (dy, h, r, gamma, d_h, dx_out, dgamma_out, ws), dy.data_ptr(), h.data_ptr(),
+            r.data_ptr(), gamma.data_ptr(), _addr(d_h), dx_out.data_ptr(), dgamma_out.data_ptr(), ws.data_ptr(),
+            ws.numel(), M, N)
     return dx_out, dgamma_out
 
 
@@ -951,12 +963,11 @@ def newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: float = 1
     _need(G, F32, "G")
     if G.dim() not in (2, 3):
         raise ValueError(f"G must be [m, n] or [batch, m, n], got shape {tuple(G.shape)}")
-    a, b, c = (float(v) for v in coeffs)
+    a, b, c = coeffs
     batch = G.shape[0] if G.dim() == 3 else 1
     m, n = G.shape[-2:]
-    out = _empty(tuple(G.shape), BF16, G) if out is None else _need(out, BF16, "out", tuple(G.shape))
-    ws = _workspace(ws, int(load_library().coda_newton_schulz_workspace_size(batch, m, n)), G)
-    with _on_one_device(G=G, out=out, ws=ws):
-        _call("coda_newton_schulz", _ptr(G), _ptr(out), batch, m, n, int(steps), a, b, c, float(eps), _ptr(ws),
-              ws.numel(), _stream())
+    out = _out(out, BF16, "out", G.shape, G)
+    ws = _workspace(ws, load_library().coda_newton_schulz_workspace_size(batch, m, n), G)
+    _launch("coda_newton_schulz", (G, out, ws), G.data_ptr(), out.data_ptr(), batch, m, n, steps, a, b, c, eps,
+            ws.data_ptr(), ws.numel())
     return out

@@ -2,42 +2,50 @@
 // does it.  For a matrix G (a gradient or a momentum):
 //
 //   X_0 = G / (|G|_F + eps)
-//   A = X X^T;  B = b A + c A^2;  X <- a X + B X        (steps times)
+//   A = X X^T;  P = a I + b A + c A^2;  X <- P X        (steps times)
 //
 // X keeps G's singular vectors and every step maps a singular value s to
 // a s + b s^3 + c s^5, which drives them all towards one.  The Gram matrix is
 // taken on the smaller side (a G with more rows than columns uses X^T X and
-// X <- a X + X B).
+// X <- X P).  Everything is a tensor-core GEMM with a fused epilogue:
+//   gram    A = X X^T                      symmetric
+//   square  P = a I + b A + c (A A)        symmetric
+//   update  X' = P X (or X P)
 //
-// Each step is three tensor-core GEMMs with fused epilogues:
-//   gram    acc = X X^T           A = acc, symmetric
-//   square  acc = A A             B = b A + c acc, symmetric
-//   update  acc = B X (or X B)    X' = a X + acc
+// Symmetry.  Only the tiles on and below the diagonal of a symmetric result are
+// computed and stored (half of the work).  A GEMM that needs a block above the
+// diagonal loads its mirror image and tells the tensor core that the operand is
+// transposed: the K-major and the MN-major form of a 64-wide k-block take the
+// same shared memory, so the choice is one tensor map and two descriptor fields
+// per k-block.
 //
-// Symmetry.  Only the tiles on and below the diagonal of A and B are computed
-// and stored (half of the work of those two GEMMs).  A GEMM that needs a block
-// above the diagonal loads its mirror image and tells the tensor core that the
-// operand is transposed: the K-major and the MN-major form of a 64-wide
-// k-block take the same shared memory, so the choice is one tensor map and two
-// descriptor fields per k-block.
+// Groups of steps.  All A and P of a matrix are polynomials of its first A, so
+// they commute, and several steps can be taken on the small side alone:
+//   A' = P A P,  Q' = P' P,  and at the end of the group X' = Q X
+// (products of commuting symmetric matrices are symmetric: half of the work
+// again).  With s and l the smaller and larger side a step alone costs
+// 3 s^2 l + s^3 operations, five of them as groups of 3 and 2 cost 6 s^2 l +
+// 14 s^3 instead of 15 s^2 l + 5 s^3.  Rounding A' instead of forming X' X'^T
+// loses the smallest singular values sooner, so a group is at most three steps,
+// later ones two, and they are only used where l is 2 or 3 times s or more.
 //
 // Precision.  Operands are fp16, not bf16: with |X|_F = 1 every value is
 // bounded, so scaled by powers of two they use fp16's 11 bits where bf16 would
 // keep 8 (same tensor-core rate).  Sums are fp32.  Two corrections keep the
 // roundings off the result where they would grow:
-//   - near the end A and B are close to multiples of the identity, and most of
-//     their norm is on the diagonal.  What fp16 drops there is kept in fp32
-//     (dA, dB: one value per row) and applied by the epilogues: 2 D A + D^2 on
-//     the diagonal of the square (off it D A is as small as the rounding of A's
-//     other entries), and (B + E) X = B X + E X;
+//   - near the end A and P are close to multiples of the identity, and most of
+//     their norm is on the diagonal.  What fp16 drops there (d) is kept in fp32
+//     beside the rounded diagonal (f) and applied by the epilogues: a product's
+//     diagonal gets d1 f2 + f1 d2 + d1 d2 (off the diagonal that is as small as
+//     the rounding of the other entries), and X' = P X + d X;
 //   - a small singular value grows by up to `a` in every step, and so does what
 //     rounding X put there.  X is therefore kept as a high and a low fp16 part;
-//     the GEMMs read the high part and the term a X both.  The last step drops
-//     the low part: nothing grows after it.
-// Against 64 bits this gives 0.5e-3 to 1.4e-3 (relative to |X|_F) for
-// Gaussian, correlated and nearly low-rank matrices, where plain bf16 products
-// give 0.9e-2 to 3e-1 and fp16 without the two corrections up to 4e-2; the
-// bf16 rounding of the output alone is 1.7e-3.
+//     the GEMMs read the high part, and the diagonal of P (all of P where X is
+//     small) multiplies the low part too.  The last update drops it.
+// Against 64 bits this gives 0.3e-3 to 1.1e-3 of |X|_F for Gaussian and
+// correlated matrices after five steps, and up to 3e-3 (in groups 7e-3) for
+// nearly low-rank ones; plain bf16 products give 0.9e-2 and 3e-1.  The bf16
+// rounding of the output alone is 1.7e-3.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -46,12 +54,12 @@
 
 namespace coda {
 
-// Powers of two the fp16 values are stored with.  Singular values stay below
-// 1.3 with the Muon coefficients, so X fits with a factor of 12 to spare and A
-// and B with a factor of 37 and 16.
+// Powers of two the fp16 values are stored with.  With the Muon coefficients
+// singular values stay below 1.3 and P below 3.5, so X fits with a factor of 12
+// to spare, A with 37, P and its products (at most 3.5^3) with 6.
 constexpr float kNsScaleX = 4096.f;
-constexpr float kNsScaleA = 1024.f;
-constexpr float kNsScaleB = 1024.f;
+constexpr float kNsScaleA = 1024.f;  // A, P A
+constexpr float kNsScaleP = 256.f;   // P, Q
 
 constexpr int kNsEpiWarps = 8;                     // two per TMEM lane quarter, each half of a tile's columns
 constexpr int kNsThreads = 64 + 32 * kNsEpiWarps;  // TMA producer, MMA issuer, epilogue warps
@@ -64,31 +72,86 @@ constexpr int kNsBars = 2 * kNsStages + 2 + 2 + 1 + 1 + 2 * kNsEpiWarps;
 constexpr int kNsSmemBytes = 1024 + kNsStages * kNsStageBytes + kNsEpiWarps * kNsEpiBytes + kNsBars * 8 + 32;
 static_assert(kNsSmemBytes <= 232448, "shared memory");
 
-enum NsKind : int { kNsGram = 0, kNsSquare, kNsUpdate };
+enum NsKind : int { kNsGram = 0, kNsSquare, kNsMul, kNsUpdate };
 
-// One of the three GEMMs, acc[i, j] = sum_k P[i, k] Q[j, k], over the batch.
+// One GEMM's tiles, acc[i, j] = sum_k P[i, k] Q[j, k], over the batch (and over
+// two products, where a phase has two).
 struct NsGeo {
   int rows, cols, nkb;    // output size of one matrix, 64-wide k-blocks
   int n_rt, n_ct, tiles;  // row tiles, column tiles, tiles of one matrix (half of them for a symmetric result)
-  int whole;              // the first `whole` tiles of the batch are one unit each,
+  int whole;              // the first `whole` tiles are one unit each,
   int rest;               // the other `rest` tiles
   int splits;             // are `splits` units each, over equal shares of the k-blocks
 };
+enum NsGeoIndex : int { kGeoGram = 0, kGeoSym, kGeoSym2, kGeoUpdate, kGeos };
+
+// The symmetric matrices: A, P, P A, and the group's product Q (two, in turn).
+enum NsBuf : int { kBufA = 0, kBufP, kBufT, kBufQ0, kBufQ1, kBufs };
 
 struct NsParams {
   // loads, 3-D [batch, y, x] with 64-wide boxes: 128 rows (K-major operand) or 64 k (MN-major)
-  CUtensorMap Xk[2], Xmn[2];  // X's high part, by step parity
-  CUtensorMap Ak, Amn, Bk, Bmn;
-  // the epilogues' boxes of 32 x 32 (64-byte swizzle): X's high and low parts, A, B, the output
-  CUtensorMap Hbox[2], Lbox[2], Abox, Bbox, Obox;
-  float* dA;  // [batch, s]: what fp16 drops of A's diagonal
-  float* dB;
-  float* part;    // partial accumulators of the split tiles
-  int* counters;  // [0]: arrivals at the grid barrier; then for each GEMM arrivals at the split tiles' parts
-  NsGeo geo[3];
+  CUtensorMap Xk[2], Xmn[2];  // X's high part, by group parity
+  CUtensorMap Sk[kBufs], Smn[kBufs];
+  // the epilogues' boxes of 32 x 32 (64-byte swizzle): X's high and low parts, the symmetric matrices, the output
+  CUtensorMap Hbox[2], Lbox[2], Sbox[kBufs], Obox;
+  float2* diag[kBufs];  // [batch, s]: (d, f): what fp16 drops of the diagonal, and the rounded diagonal
+  float* part;          // partial accumulators of the split tiles
+  int* counters;        // [0]: arrivals at the grid barrier; then for each geometry arrivals at the split tiles' parts
+  NsGeo geo[kGeos];
   int batch, steps, tall;
+  int first, later;     // steps of the first group and of later ones, at most
   float a, b, c;
   uint64_t wait_ns;
+};
+
+// The phases of a group of one, two or three steps, with a grid barrier after
+// each.  A phase is a GEMM (or two products side by side: `two`) given by its
+// symmetric matrices: left, right, result.
+struct NsPhase {
+  uint8_t kind, two;
+  uint8_t l, r, out;
+  uint8_t l2, r2, out2;
+};
+__device__ constexpr NsPhase kNsPhases[3][10] = {
+    {{kNsGram, 0, 0, 0, kBufA, 0, 0, 0}, {kNsSquare, 0, kBufA, kBufA, kBufQ0, 0, 0, 0},
+     {kNsUpdate, 0, kBufQ0, 0, 0, 0, 0, 0}},
+    {{kNsGram, 0, 0, 0, kBufA, 0, 0, 0}, {kNsSquare, 0, kBufA, kBufA, kBufQ0, 0, 0, 0},
+     {kNsMul, 0, kBufQ0, kBufA, kBufT, 0, 0, 0}, {kNsMul, 0, kBufT, kBufQ0, kBufA, 0, 0, 0},
+     {kNsSquare, 0, kBufA, kBufA, kBufP, 0, 0, 0}, {kNsMul, 0, kBufP, kBufQ0, kBufQ1, 0, 0, 0},
+     {kNsUpdate, 0, kBufQ1, 0, 0, 0, 0, 0}},
+    {{kNsGram, 0, 0, 0, kBufA, 0, 0, 0}, {kNsSquare, 0, kBufA, kBufA, kBufQ0, 0, 0, 0},
+     {kNsMul, 0, kBufQ0, kBufA, kBufT, 0, 0, 0}, {kNsMul, 0, kBufT, kBufQ0, kBufA, 0, 0, 0},
+     {kNsSquare, 0, kBufA, kBufA, kBufP, 0, 0, 0}, {kNsMul, 1, kBufP, kBufA, kBufT, kBufP, kBufQ0, kBufQ1},
+     {kNsMul, 0, kBufT, kBufP, kBufA, 0, 0, 0}, {kNsSquare, 0, kBufA, kBufA, kBufP, 0, 0, 0},
+     {kNsMul, 0, kBufP, kBufQ1, kBufQ0, 0, 0, 0}, {kNsUpdate, 0, kBufQ0, 0, 0, 0, 0, 0}},
+};
+__device__ constexpr int kNsPhaseCount[3] = {3, 7, 10};
+
+// Walks the phases; every role of every CTA takes the same ones.
+struct NsSeq {
+  int ph = -1;     // phases begun, less one
+  int group = 0;   // X of this group is in buffer group & 1
+  int left, size;  // steps left, this group's included; its steps
+  int pos = -1;
+  NsPhase f;
+  __device__ __forceinline__ explicit NsSeq(const NsParams& p) : left(p.steps), size(min(p.first, p.steps)) {}
+  __device__ __forceinline__ bool next(const NsParams& p) {
+    ++ph;
+    if (++pos == kNsPhaseCount[size - 1]) {
+      left -= size;
+      if (left == 0) return false;
+      ++group;
+      size = min(p.later, left);
+      pos = 0;
+    }
+    f = kNsPhases[size - 1][pos];
+    return true;
+  }
+  __device__ __forceinline__ bool last_group() const { return left == size; }
+  __device__ __forceinline__ bool last_phase() const { return left == size && f.kind == kNsUpdate; }
+  __device__ __forceinline__ int geo() const {
+    return f.kind == kNsGram ? kGeoGram : (f.kind == kNsUpdate ? kGeoUpdate : (f.two ? kGeoSym2 : kGeoSym));
+  }
 };
 
 // 3-D tiled copies (x, y, batch).
@@ -190,9 +253,9 @@ __device__ __forceinline__ int add_acq_rel_cta(int* addr, int v) {
   return old;
 }
 
-// A unit of work: a tile (matrix, row tile, column tile) and its k-blocks.
+// A unit of work: a tile (product, matrix, row tile, column tile) and its k-blocks.
 struct NsUnit {
-  int bz, rt, ct;
+  int job, bz, rt, ct;
   int kb0, kb1;
   int part;   // which of a split tile's parts (-1: a whole tile)
   int split;  // the split tile's number
@@ -202,7 +265,7 @@ struct NsUnit {
 // i starts at tile i (i + 1) / 2.  Otherwise the tiles that share the longer
 // side's operand follow each other.
 template <bool SYM>
-__device__ __forceinline__ NsUnit ns_unit(const NsGeo& g, int u) {
+__device__ __forceinline__ NsUnit ns_unit_of(const NsGeo& g, int batch, int u) {
   NsUnit n;
   int t = u;
   n.part = -1;
@@ -221,6 +284,8 @@ __device__ __forceinline__ NsUnit ns_unit(const NsGeo& g, int u) {
   }
   n.bz = t / g.tiles;
   t -= n.bz * g.tiles;
+  n.job = n.bz >= batch ? 1 : 0;
+  n.bz -= n.job * batch;
   if (SYM) {
     int i = static_cast<int>((sqrtf(8.f * static_cast<float>(t) + 1.f) - 1.f) * 0.5f);
     while (i * (i + 1) / 2 > t) --i;
@@ -237,28 +302,36 @@ __device__ __forceinline__ NsUnit ns_unit(const NsGeo& g, int u) {
   return n;
 }
 
-__device__ __forceinline__ NsUnit ns_unit(const NsParams& p, int kind, int u) {
-  return kind == kNsUpdate ? ns_unit<false>(p.geo[kind], u) : ns_unit<true>(p.geo[kind], u);
+__device__ __forceinline__ NsUnit ns_unit(const NsParams& p, const NsSeq& s, int u) {
+  const int g = s.geo();
+  return g == kGeoUpdate ? ns_unit_of<false>(p.geo[g], p.batch, u) : ns_unit_of<true>(p.geo[g], p.batch, u);
 }
 
-// An operand of one GEMM: its two views, and whether the k-block at k0 of the
-// rows of tile `t` is loaded [k, row] (the MN-major view).
+__device__ __forceinline__ int ns_units(const NsParams& p, const NsSeq& s) {
+  const NsGeo& g = p.geo[s.geo()];
+  return g.whole + g.rest * g.splits;
+}
+
+// An operand of one GEMM: its two views, and whether the k-block kb of the rows
+// of tile `t` is loaded [k, row] (the MN-major view).
 struct NsOperand {
   const CUtensorMap *k, *mn;
-  int sym;  // A or B: blocks of the tile's size on and below the diagonal are stored
+  int sym;  // blocks of the tile's size on and below the diagonal are stored
   __device__ __forceinline__ bool is_mn(int t, int kb, int tile) const { return sym ? kb * 64 / tile > t : mn != nullptr; }
 };
 
-__device__ __forceinline__ void ns_operands(const NsParams& p, int kind, int par, NsOperand& P, NsOperand& Q) {
-  const NsOperand xk{&p.Xk[par], nullptr, 0}, xm{nullptr, &p.Xmn[par], 0};
-  if (kind == kNsGram) {
+__device__ __forceinline__ void ns_operands(const NsParams& p, const NsSeq& s, int job, NsOperand& P, NsOperand& Q) {
+  const int par = s.group & 1;
+  const int l = job ? s.f.l2 : s.f.l, r = job ? s.f.r2 : s.f.r;
+  const NsOperand xk{&p.Xk[par], nullptr, 0}, xm{nullptr, &p.Xmn[par], 0}, sl{&p.Sk[l], &p.Smn[l], 1};
+  if (s.f.kind == kNsGram) {
     P = Q = p.tall ? xm : xk;
-  } else if (kind == kNsSquare) {
-    P = Q = NsOperand{&p.Ak, &p.Amn, 1};
+  } else if (s.f.kind == kNsUpdate) {
+    P = p.tall ? xk : sl;
+    Q = p.tall ? sl : xm;
   } else {
-    const NsOperand bs{&p.Bk, &p.Bmn, 1};
-    P = p.tall ? xk : bs;
-    Q = p.tall ? bs : xm;
+    P = sl;
+    Q = NsOperand{&p.Sk[r], &p.Smn[r], 1};
   }
 }
 
@@ -297,28 +370,36 @@ __device__ __forceinline__ void ns_add4(uint32_t (&v)[32], int j, const float4& 
 // and bound the update at 20 us a tile.)  Sixteen warps with a quarter of the
 // columns each, or tensor-memory loads of 8 columns in a small loop, were
 // slower.  Returns false if a wait gave up.
+// KIND kNsGram: gram or product (a product has a correction on the diagonal).
 template <int KIND, bool PAIR>
-__device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, int k, int acc, uint32_t parity,
-                                            uint64_t* tfull, NsEpi& e, const WaitCtx& w) {
+__device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, const NsUnit& n, int gen, int acc,
+                                            uint32_t parity, uint64_t* tfull, NsEpi& e, const WaitCtx& w) {
   constexpr int kTile = PAIR ? 256 : 128;
   constexpr int kHalf = kTile / 2;  // columns of this warp
   constexpr int kBlks = kHalf / 32;
-  const NsGeo& g = p.geo[KIND];
-  const bool last = k + 1 == p.steps;
-  const bool has_low = KIND == kNsUpdate && k + 2 < p.steps;  // the result's low part is stored
-  const bool in_low = KIND == kNsUpdate && !last;             // X has one
-  const CUtensorMap* in0 = KIND == kNsSquare ? &p.Abox : &p.Hbox[k & 1];
-  const CUtensorMap* in1 = &p.Lbox[k & 1];
+  const int gi = s.geo();
+  const NsGeo& g = p.geo[gi];
+  const int buf_l = n.job ? s.f.l2 : s.f.l, buf_r = n.job ? s.f.r2 : s.f.r, buf_out = n.job ? s.f.out2 : s.f.out;
+  const int par = s.group & 1;
+  const bool last = s.last_group();
+  const bool in_low = KIND == kNsUpdate && (!last || s.group == 0);  // X has a low part
+  const bool has_low = KIND == kNsUpdate && s.left > s.size && s.left - s.size > min(p.later, s.left - s.size);
+  const CUtensorMap* in0 = KIND == kNsSquare ? &p.Sbox[kBufA] : &p.Hbox[par];
+  const CUtensorMap* in1 = &p.Lbox[par];
   const int lane = e.lane;
   const int row0 = n.rt * kTile + e.rank * 128 + e.q * 32;
   const int row = row0 + lane;
   const int col0 = n.ct * kTile + e.half * kHalf;
   const bool live = row < g.rows;
-  // dA of the row (square); dB of the row of B X, of the column of X B (update).
-  // Written by other CTAs of this launch: read through L2.
+  // The diagonal of P: of the row of P X, of the column of X P.  Written by
+  // other CTAs of this launch: read through L2.
   const bool by_col = KIND == kNsUpdate && p.tall;
-  const float* dv = (KIND == kNsSquare ? p.dA : p.dB) + static_cast<size_t>(n.bz) * (by_col ? g.cols : g.rows);
-  const float di = KIND != kNsGram && !by_col && live ? __ldcg(dv + row) : 0.f;
+  const float2* dv = p.diag[buf_l] + static_cast<size_t>(n.bz) * (by_col ? g.cols : g.rows);
+  float2 di = make_float2(0.f, 0.f);  // (d, f + d) of the row
+  if (KIND == kNsUpdate && !by_col && live) {
+    di = __ldcg(dv + row);
+    di.y += di.x;
+  }
   int nblk = (g.cols - col0 + 31) / 32;
   if (nblk > kBlks) nblk = kBlks;
   if (row0 >= g.rows || nblk < 0) nblk = 0;  // (uniform over the warp)
@@ -328,7 +409,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
     b0 = n.part * (kBlks / g.splits);
     b1 = min(nblk, b0 + kBlks / g.splits);
   }
-  float dc = 0.f;  // a + d of the block's column number `lane`
+  float2 dc = make_float2(0.f, 0.f);  // (d, f + d) of the block's column number `lane`
   auto fetch = [&](int b, uint32_t cnt) {
     if (KIND == kNsGram) return;
     const int c = col0 + b * 32;
@@ -339,7 +420,10 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
       tma_load_3d(d, in0, &e.bars[cnt & 1], c, row0, n.bz);
       if (in_low) tma_load_3d(d + kNsBoxBytes, in1, &e.bars[cnt & 1], c, row0, n.bz);
     }
-    if (by_col) dc = p.a + (c + lane < g.cols ? __ldcg(dv + c + lane) : 0.f);
+    if (by_col && c + lane < g.cols) {
+      dc = __ldcg(dv + c + lane);
+      dc.y += dc.x;
+    }
   };
   if (b0 < b1) fetch(b0, e.cnt);
   // Warp-uniform outcomes: tcgen05.ld below is a warp-collective instruction.
@@ -372,25 +456,25 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
     __syncwarp();
     int ok = 1;
     if (lane == 0) {
-      int* c = p.counters + 1 + KIND * kNsSplitCounters + n.split * (PAIR ? 16 : 8) + region;
+      int* c = p.counters + 1 + gi * kNsSplitCounters + n.split * (PAIR ? 16 : 8) + region;
       red_release_add(c, 1);
-      if (b0 < b1) ok = ns_count_wait(c, g.splits * (k + 1), w) ? 1 : 0;
+      if (b0 < b1) ok = ns_count_wait(c, g.splits * (gen + 1), w) ? 1 : 0;
     }
     __syncwarp();
     if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
   }
-  // the accumulator's share: gram S_A / S_X^2, square c S_B / S_A^2, update 1 / S_B
-  const float sc = KIND == kNsGram ? kNsScaleA / (kNsScaleX * kNsScaleX)
-                                   : (KIND == kNsSquare ? p.c * (kNsScaleB / (kNsScaleA * kNsScaleA)) : 1.f / kNsScaleB);
-  // the input's: square b S_B / S_A, update a + d of the row
-  const float si = KIND == kNsSquare ? p.b * (kNsScaleB / kNsScaleA) : p.a + di;
+  // the result's scale, and the accumulator's share of it
+  const float so = buf_out == kBufA || buf_out == kBufT ? kNsScaleA : kNsScaleP;
+  const float sc = KIND == kNsSquare ? p.c * (kNsScaleP / (kNsScaleA * kNsScaleA))
+                                     : (KIND == kNsGram && s.f.kind == kNsGram ? kNsScaleA / (kNsScaleX * kNsScaleX)
+                                                                              : 1.f / kNsScaleP);
 #pragma unroll 1
   for (int b = b0; b < b1; ++b, ++e.cnt) {
     const int c32 = col0 + b * 32;
     const int buf = e.cnt & 1;
     uint8_t* S0 = e.stg + buf * (2 * kNsBoxBytes);
     uint8_t* S1 = S0 + kNsBoxBytes;
-    const float dcb = dc;
+    const float2 dcb = dc;
     if (KIND == kNsGram) {
       if (lane == 0) bulk_wait_read<1>();
       __syncwarp();
@@ -439,30 +523,42 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) in[4 * j + i] = f2_half(w0[i]);
       }
-      if (in_low) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w1[4] = {x1[j].x, x1[j].y, x1[j].z, x1[j].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) in[4 * j + i] = f2_add(in[4 * j + i], f2_half(w1[i]));
-        }
-      }
-      if (by_col) {
+      if (KIND == kNsSquare) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          r[i] = f2_fma(in[i], f2_set(__shfl_sync(0xffffffffu, dcb, 2 * i), __shfl_sync(0xffffffffu, dcb, 2 * i + 1)),
-                        r[i]);
-      } else {
+          r[i] = f2_fma(in[i], f2_set(p.b * (kNsScaleP / kNsScaleA), p.b * (kNsScaleP / kNsScaleA)), r[i]);
+      } else {  // d X + (f + d) (X's low part)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = f2_fma(in[i], f2_set(si, si), r[i]);
+        for (int i = 0; i < 16; ++i) {
+          uint64_t d = f2_set(di.x, di.x);
+          if (by_col)
+            d = f2_set(__shfl_sync(0xffffffffu, dcb.x, 2 * i), __shfl_sync(0xffffffffu, dcb.x, 2 * i + 1));
+          r[i] = f2_fma(in[i], d, r[i]);
+        }
+        if (in_low) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w1[4] = {x1[j].x, x1[j].y, x1[j].z, x1[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = 4 * j + i;
+              uint64_t q = f2_set(di.y, di.y);
+              if (by_col)
+                q = f2_set(__shfl_sync(0xffffffffu, dcb.y, 2 * at), __shfl_sync(0xffffffffu, dcb.y, 2 * at + 1));
+              r[at] = f2_fma(f2_half(w1[i]), q, r[at]);
+            }
+          }
+        }
       }
     }
     if (KIND != kNsUpdate && c32 == row0) {
       // the block of this row's diagonal entry, column `lane`
       float corr = 0.f, dval = 0.f;
-      if (KIND == kNsSquare) {  // b d + c (2 d A + d^2)
-        const __half f = *reinterpret_cast<const __half*>(S0 + sw64_off(lane, lane >> 3) + (lane & 7) * 2);
-        corr = di * fmaf(p.c, fmaf(2.f / kNsScaleA, __half2float(f), di), p.b) * kNsScaleB;
+      const size_t at = static_cast<size_t>(n.bz) * g.rows + (live ? row : 0);
+      if (s.f.kind != kNsGram) {
+        const float2 l = __ldcg(p.diag[buf_l] + at), q = __ldcg(p.diag[buf_r] + at);
+        corr = fmaf(l.x, q.y, fmaf(l.y, q.x, l.x * q.x)) * so;
+        if (KIND == kNsSquare) corr = fmaf(p.c, corr, fmaf(p.b, l.x, p.a) * so);
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -472,9 +568,8 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
         dval = lane == 2 * i ? x.x : (lane == 2 * i + 1 ? x.y : dval);
         r[i] = f2_set(x.x, x.y);
       }
-      if (live)
-        (KIND == kNsGram ? p.dA : p.dB)[static_cast<size_t>(n.bz) * g.rows + row] =
-            (dval - __half2float(__float2half_rn(dval))) * (KIND == kNsGram ? 1.f / kNsScaleA : 1.f / kNsScaleB);
+      const float f = __half2float(__float2half_rn(dval));
+      if (live) p.diag[buf_out][at] = make_float2((dval - f) / so, f / so);
     }
     uint32_t o[16];
     if (KIND == kNsUpdate && last) {
@@ -506,10 +601,9 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsUnit& n, 
     fence_async_smem();
     __syncwarp();
     if (lane == 0) {
-      const CUtensorMap* m = KIND == kNsGram ? &p.Abox
-                                             : (KIND == kNsSquare ? &p.Bbox : (last ? &p.Obox : &p.Hbox[(k + 1) & 1]));
+      const CUtensorMap* m = KIND != kNsUpdate ? &p.Sbox[buf_out] : (last ? &p.Obox : &p.Hbox[par ^ 1]);
       tma_store_3d(m, S0, c32, row0, n.bz);
-      if (has_low) tma_store_3d(&p.Lbox[(k + 1) & 1], S1, c32, row0, n.bz);
+      if (has_low) tma_store_3d(&p.Lbox[par ^ 1], S1, c32, row0, n.bz);
       bulk_commit();
     }
   }
@@ -548,7 +642,6 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const int step = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
   const int first = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
-  const int phases = 3 * p.steps;
   const int arrivals = static_cast<int>(gridDim.x);  // per phase
 
   if (threadIdx.x == 0) {
@@ -590,18 +683,17 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       long issued = 0;
       bool ok = true;
       const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
-      for (int ph = 0; ok && ph < phases; ++ph) {
-        const int kind = ph % 3;
-        NsOperand op[2];
-        ns_operands(p, kind, (ph / 3) & 1, op[0], op[1]);
-        const int nunits = p.geo[kind].whole + p.geo[kind].rest * p.geo[kind].splits;
-        if (ph > 0) {
-          if (!ns_count_wait(p.counters, arrivals * ph, w)) break;
+      for (NsSeq s(p); ok && s.next(p);) {
+        const int nunits = ns_units(p, s);
+        if (s.ph > 0) {
+          if (!ns_count_wait(p.counters, arrivals * s.ph, w)) break;
           fence_proxy_async_global();  // the loads below see what other CTAs' copies wrote
           mbar_arrive(go);
         }
         for (int u = first; ok && u < nunits; u += step) {
-          const NsUnit n = ns_unit(p, kind, u);
+          const NsUnit n = ns_unit(p, s, u);
+          NsOperand op[2];
+          ns_operands(p, s, n.job, op[0], op[1]);
           for (int kb = n.kb0; kb < n.kb1; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
               ok = false;
@@ -658,13 +750,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       uint32_t phase = 0;
       int it = 0;
       bool ok = true;
-      for (int ph = 0; ok && ph < phases; ++ph) {
-        const int kind = ph % 3;
-        NsOperand P, Q;
-        ns_operands(p, kind, (ph / 3) & 1, P, Q);
-        const int nunits = p.geo[kind].whole + p.geo[kind].rest * p.geo[kind].splits;
+      for (NsSeq s(p); ok && s.next(p);) {
+        const int nunits = ns_units(p, s);
         for (int u = first; ok && u < nunits; u += step, ++it) {
-          const NsUnit n = ns_unit(p, kind, u);
+          const NsUnit n = ns_unit(p, s, u);
+          NsOperand P, Q;
+          ns_operands(p, s, n.job, P, Q);
           const int acc = it & 1;
           if (!mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, w)) {
             ok = false;
@@ -732,22 +823,24 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
     int it = 0;
     bool ok = true;
-    for (int ph = 0; ok && ph < phases; ++ph) {
-      const int kind = ph % 3, k = ph / 3;
-      const int nunits = p.geo[kind].whole + p.geo[kind].rest * p.geo[kind].splits;
+    uint64_t gens = 0;  // phases of each geometry so far, 16 bits each
+    for (NsSeq s(p); ok && s.next(p);) {
+      const int nunits = ns_units(p, s);
+      const int gen = static_cast<int>(gens >> (16 * s.geo())) & 0xffff;
+      gens += 1ull << (16 * s.geo());
       // (also without a unit: an arrival must not come before the previous barrier)
-      if (ph > 0 && !__all_sync(0xffffffffu, mbar_wait(go, (ph - 1) & 1, w))) break;
+      if (s.ph > 0 && !__all_sync(0xffffffffu, mbar_wait(go, (s.ph - 1) & 1, w))) break;
       if (lane == 0) fence_proxy_async_global();
       for (int u = first; ok && u < nunits; u += step, ++it) {
-        const NsUnit n = ns_unit(p, kind, u);
+        const NsUnit n = ns_unit(p, s, u);
         const int acc = it & 1;
         const uint32_t par = (it >> 1) & 1;
-        if (kind == kNsGram)
-          ok = ns_epilogue<kNsGram, PAIR>(p, n, k, acc, par, tfull, e, w);
-        else if (kind == kNsSquare)
-          ok = ns_epilogue<kNsSquare, PAIR>(p, n, k, acc, par, tfull, e, w);
+        if (s.f.kind == kNsSquare)
+          ok = ns_epilogue<kNsSquare, PAIR>(p, s, n, gen, acc, par, tfull, e, w);
+        else if (s.f.kind == kNsUpdate)
+          ok = ns_epilogue<kNsUpdate, PAIR>(p, s, n, gen, acc, par, tfull, e, w);
         else
-          ok = ns_epilogue<kNsUpdate, PAIR>(p, n, k, acc, par, tfull, e, w);
+          ok = ns_epilogue<kNsGram, PAIR>(p, s, n, gen, acc, par, tfull, e, w);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -766,7 +859,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       __syncwarp();
       // the CTA's last warp arrives for all of them: its release covers what the
       // others' lanes wrote before the warp barrier and their arrivals here
-      if (lane == 0 && ph + 1 < phases && add_acq_rel_cta(warps_done, 1) == kNsEpiWarps * (ph + 1) - 1)
+      if (lane == 0 && !s.last_phase() && add_acq_rel_cta(warps_done, 1) == kNsEpiWarps * (s.ph + 1) - 1)
         red_release_add(p.counters, 1);
     }
     if (lane == 0) bulk_wait_all<0>();
@@ -842,9 +935,11 @@ __global__ void __launch_bounds__(kNsNormThreads) ns_scale_kernel(const float* _
   const float f2 = static_cast<float>(f / static_cast<double>(f1));
   const size_t off = static_cast<size_t>(blockIdx.y) * n8;
   const float4* g = reinterpret_cast<const float4*>(G) + off * 2;
-  for (size_t i = blockIdx.x * static_cast<size_t>(kNsNormThreads) + threadIdx.x; i < n8;
-       i += static_cast<size_t>(gridDim.x) * kNsNormThreads) {
-    const float4 a = __ldg(g + 2 * i), b = __ldg(g + 2 * i + 1);
+  // from the end, which the sums have read last and left in L2
+  for (size_t r = blockIdx.x * static_cast<size_t>(kNsNormThreads) + threadIdx.x; r < n8;
+       r += static_cast<size_t>(gridDim.x) * kNsNormThreads) {
+    const size_t i = n8 - 1 - r;
+    const float4 a = __ldcs(g + 2 * i), b = __ldcs(g + 2 * i + 1);
     const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t h[4], l[4];
 #pragma unroll
@@ -855,7 +950,7 @@ __global__ void __launch_bounds__(kNsNormThreads) ns_scale_kernel(const float* _
       l[e] = pack_f16x2(x0 - hf.x, x1 - hf.y);
     }
     reinterpret_cast<uint4*>(hi)[off + i] = make_uint4(h[0], h[1], h[2], h[3]);
-    if (lo != nullptr) reinterpret_cast<uint4*>(lo)[off + i] = make_uint4(l[0], l[1], l[2], l[3]);
+    reinterpret_cast<uint4*>(lo)[off + i] = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 

@@ -103,15 +103,16 @@ inline int norm8_bwd_blocks(int64_t M, int64_t N) {
 
 // ------------------------------------------------------------ Newton-Schulz
 
-constexpr int kNsMaxNormBlocks = 512;
+constexpr int kNsMaxNormBlocks = 1184;  // eight for each of 148 SMs
 
-constexpr int kNsMaxCounters = 1 + 3 * kNsSplitCounters;
+constexpr int kNsMaxCounters = 1 + kGeos * kNsSplitCounters;
 
 struct NsPlan {
   int64_t batch, m, n, s;  // s: the smaller side
   bool tall, pair;         // pair: 256 x 256 tiles on CTA pairs, else 128 x 128
+  bool grouped;            // steps in groups of up to three
   int norm_blocks;
-  size_t hi[2], lo[2], A, B, dA, dB, sums, counters, part, bytes;
+  size_t hi[2], lo[2], sym[kBufs], diag[kBufs], sums, counters, part, bytes;
 };
 
 inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
@@ -125,6 +126,10 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
   // of the 74 pairs: 224 against 237 us at 1024 x 4096 (64 tiles); with fewer,
   // four times as many small tiles end sooner: 157 against 194 us at 1024 x 1024.
   p.pair = p.s >= 512 && batch * ((m + 255) / 256) * ((n + 255) / 256) >= 48;
+  // Groups save 9 s^2 l operations of five steps and cost 9 s^3 and two more
+  // phases: 650 against 1060 us at 2048 x 16384, 322 against 368 at 2048 x 4096
+  // (pairs), but 174 against 169 at 1024 x 2048 and 278 against 266 at 2048 x 2048.
+  p.grouped = (p.tall ? m : n) >= (p.pair ? 2 : 3) * p.s;
   const int64_t n8 = m * n / 8;
   p.norm_blocks = static_cast<int>(std::min<int64_t>(kNsMaxNormBlocks, (n8 + 2047) / 2048));
   size_t o = 0;
@@ -137,10 +142,11 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
     p.hi[i] = take(static_cast<size_t>(batch) * m * n * 2);
     p.lo[i] = take(static_cast<size_t>(batch) * m * n * 2);
   }
-  p.A = take(static_cast<size_t>(batch) * p.s * p.s * 2);
-  p.B = take(static_cast<size_t>(batch) * p.s * p.s * 2);
-  p.dA = take(static_cast<size_t>(batch) * p.s * 4);
-  p.dB = take(static_cast<size_t>(batch) * p.s * 4);
+  for (int i = 0; i < kBufs; ++i) {
+    const bool used = p.grouped || i == kBufA || i == kBufQ0;
+    p.sym[i] = take(used ? static_cast<size_t>(batch) * p.s * p.s * 2 : 0);
+    p.diag[i] = take(used ? static_cast<size_t>(batch) * p.s * 8 : 0);
+  }
   p.sums = take(static_cast<size_t>(batch) * p.norm_blocks * 8);
   p.counters = take(kNsMaxCounters * 4);
   // at most one split unit per CTA (pair) of the grid
@@ -223,9 +229,10 @@ coda_status_t ns_launch(int dev, DevInfo* info, NsParams& p, const NsPlan& pl, c
     }
   }
   const int64_t s = pl.s, l = pl.tall ? pl.m : pl.n;
-  p.geo[kNsGram] = ns_geo(pl.batch, s, s, l, true, kTile, slots[dev]);
-  p.geo[kNsSquare] = ns_geo(pl.batch, s, s, s, true, kTile, slots[dev]);
-  p.geo[kNsUpdate] = ns_geo(pl.batch, pl.m, pl.n, s, false, kTile, slots[dev]);
+  p.geo[kGeoGram] = ns_geo(pl.batch, s, s, l, true, kTile, slots[dev]);
+  p.geo[kGeoSym] = ns_geo(pl.batch, s, s, s, true, kTile, slots[dev]);
+  p.geo[kGeoSym2] = ns_geo(2 * pl.batch, s, s, s, true, kTile, slots[dev]);
+  p.geo[kGeoUpdate] = ns_geo(pl.batch, pl.m, pl.n, s, false, kTile, slots[dev]);
   int n = 0;
   for (const NsGeo& g : p.geo) n = std::max(n, g.whole > 0 ? slots[dev] : g.rest * g.splits);
   p.wait_ns = static_cast<uint64_t>(g_wait_ns);
@@ -399,7 +406,7 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
   if (batch == 0) return CODA_OK;
   const NsPlan pl = ns_plan(batch, m, n);
   CODA_CHECK(ws && ws_bytes >= pl.bytes, CODA_ERR_WORKSPACE);
-  CODA_CHECK(batch * ((m + 127) / 128) * ((n + 127) / 128) <= kMaxInt, CODA_ERR_SHAPE);
+  CODA_CHECK(2 * batch * ((m + 127) / 128) * ((n + 127) / 128) <= kMaxInt, CODA_ERR_SHAPE);
   int dev;
   DevInfo* info;
   coda_status_t st = current_device(&dev, &info);
@@ -410,15 +417,14 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
   NsParams p{};
   __half* hi[2] = {reinterpret_cast<__half*>(w + pl.hi[0]), reinterpret_cast<__half*>(w + pl.hi[1])};
   __half* lo[2] = {reinterpret_cast<__half*>(w + pl.lo[0]), reinterpret_cast<__half*>(w + pl.lo[1])};
-  __half* A = reinterpret_cast<__half*>(w + pl.A);
-  __half* B = reinterpret_cast<__half*>(w + pl.B);
-  p.dA = reinterpret_cast<float*>(w + pl.dA);
-  p.dB = reinterpret_cast<float*>(w + pl.dB);
+  for (int i = 0; i < kBufs; ++i) p.diag[i] = reinterpret_cast<float2*>(w + pl.diag[i]);
   p.part = reinterpret_cast<float*>(w + pl.part);
   p.counters = reinterpret_cast<int*>(w + pl.counters);
   p.batch = static_cast<int>(batch);
   p.steps = steps;
   p.tall = pl.tall ? 1 : 0;
+  p.first = pl.grouped ? 3 : 1;
+  p.later = pl.grouped ? 2 : 1;
   p.a = a;
   p.b = b;
   p.c = c;
@@ -427,10 +433,13 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
   for (int i = 0; i < 2; ++i)
     ok = ok && tmap3d(&p.Xk[i], hi[i], false, n, m, batch, 128) && tmap3d(&p.Xmn[i], hi[i], false, n, m, batch, 64) &&
          tmap3d(&p.Hbox[i], hi[i], false, n, m, batch, 32, 32) && tmap3d(&p.Lbox[i], lo[i], false, n, m, batch, 32, 32);
-  ok = ok && tmap3d(&p.Ak, A, false, s, s, batch, 128) && tmap3d(&p.Amn, A, false, s, s, batch, 64) &&
-       tmap3d(&p.Abox, A, false, s, s, batch, 32, 32) && tmap3d(&p.Bk, B, false, s, s, batch, 128) &&
-       tmap3d(&p.Bmn, B, false, s, s, batch, 64) && tmap3d(&p.Bbox, B, false, s, s, batch, 32, 32) &&
-       tmap3d(&p.Obox, out, true, n, m, batch, 32, 32);
+  for (int i = 0; i < kBufs; ++i) {
+    if (!pl.grouped && i != kBufA && i != kBufQ0) continue;
+    const void* b = w + pl.sym[i];
+    ok = ok && tmap3d(&p.Sk[i], b, false, s, s, batch, 128) && tmap3d(&p.Smn[i], b, false, s, s, batch, 64) &&
+         tmap3d(&p.Sbox[i], b, false, s, s, batch, 32, 32);
+  }
+  ok = ok && tmap3d(&p.Obox, out, true, n, m, batch, 32, 32);
   if (!ok) return CODA_ERR_INTERNAL;
   const size_t n8 = static_cast<size_t>(m) * n / 8;
   st = launch_pdl(ns_sumsq_kernel, dim3(static_cast<unsigned>(pl.norm_blocks), static_cast<unsigned>(batch)),
@@ -438,7 +447,7 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
   if (st != CODA_OK) return st;
   st = launch_pdl(ns_scale_kernel, dim3(static_cast<unsigned>(pl.norm_blocks), static_cast<unsigned>(batch)),
                   kNsNormThreads, 0, 0, stm, G, n8, pl.norm_blocks, static_cast<const double*>(sums),
-                  static_cast<double>(eps), hi[0], steps > 1 ? lo[0] : static_cast<__half*>(nullptr), p.counters,
+                  static_cast<double>(eps), hi[0], lo[0], p.counters,
                   kNsMaxCounters);
   if (st != CODA_OK) return st;
   return pl.pair ? ns_launch<true>(dev, info, p, pl, stm) : ns_launch<false>(dev, info, p, pl, stm);
