@@ -82,7 +82,7 @@ _SIGS = {
     "coda_gemm_res_partialrms_mx": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
     "coda_gemm_rowscale_partial_mx": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _F, _P, _P, _I64, _I64, _I64, _P]),
     "coda_embed": (_ST, [_P, _P, _F, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
-    "coda_embed_bwd_workspace_size": (_SZ, [_I64, _I64]),
+    "coda_embed_bwd_workspace_size": (_SZ, [_I64, _I64, _I64]),
     "coda_embed_bwd": (_ST, [_P, _P, _F, _P, ctypes.c_int, _P, _SZ, _I64, _I64, _I64, _P]),
     "coda_add_rmsnorm_mx": (_ST, [_P, _P, _P, _F, _P, _P, _P, _P, _I64, _I64, _P]),
     "coda_add_rmsnorm_fp8": (_ST, [_P, _P, _P, _F, _P, _P, _P, _P, _P, _I64, _I64, _P]),
@@ -892,7 +892,7 @@ def embed_bwd(tokens, dh, V: int, scale: float = 1.0, dE_out=None, accumulate: b
     if accumulate and dE_out is None:
         raise ValueError("accumulate needs dE_out")
     dE_out = _out(dE_out, F32, "dE_out", (V, D), dh)
-    ws = _workspace(ws, load_library().coda_embed_bwd_workspace_size(M, D), dh)
+    ws = _workspace(ws, load_library().coda_embed_bwd_workspace_size(M, D, V), dh)
     _launch("coda_embed_bwd", (dh, tokens, dE_out, ws), tokens.data_ptr(), dh.data_ptr(), scale, dE_out.data_ptr(),
             1 if accumulate else 0, ws.data_ptr(), ws.numel(), M, D, V)
     return dE_out

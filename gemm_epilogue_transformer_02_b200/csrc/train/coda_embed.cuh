@@ -81,12 +81,14 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embed_kernel(
 //
 // 1. embed_sort_kernel: the (token, row) pairs in order of token, rows of one
 //    token in increasing order (a least-significant-digit radix sort, which is
-//    stable).  One cluster of eight CTAs sorts; the others meanwhile fill dE
-//    with zeros, the larger part of the traffic.
+//    stable), by one cluster of eight CTAs, and a bitmap of the tokens that
+//    occur.  The other clusters meanwhile fill the first rows of dE with zeros.
 // 2. embed_bwd_kernel: each block takes `chunk` consecutive pairs, whatever
 //    their tokens, so a token that fills half of the batch costs no more than
 //    distinct ones.  A token's run inside one chunk is summed and written; the
-//    sums of a run that crosses a chunk's border go to the workspace.
+//    sums of a run that crosses a chunk's border go to the workspace.  Other
+//    blocks write zeros to dE's remaining rows whose tokens do not occur: they
+//    are most of the traffic, and overlap the sums.
 // 3. embed_bwd_join_kernel: adds a crossing run's parts in order.
 // Every sum has one order, given by the tokens alone: no atomics on values.
 
@@ -102,21 +104,51 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
   return v;
 }
 
+// Writes `len` zero bytes (a multiple of 16) to dst as bulk copies of at most
+// kZeroPiece from a zeroed shared buffer, by one thread; the copies are left in
+// flight (bulk_wait_all before the block ends).
+constexpr int kZeroPiece = 16384;
+
+__device__ __forceinline__ void zero_run(uint8_t* dst, size_t len, const void* zeros) {
+  for (size_t o = 0; o < len; o += kZeroPiece) {
+    const uint32_t n = static_cast<uint32_t>(len - o < kZeroPiece ? len - o : kZeroPiece);
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + o), "r"(smem_u32(zeros)),
+                 "r"(n)
+                 : "memory");
+    bulk_commit();
+    bulk_wait_read<8>();
+  }
+}
+
+__device__ __forceinline__ void zero_buffer(void* buf) {
+  for (int i = threadIdx.x; i < kZeroPiece / 16; i += blockDim.x)
+    reinterpret_cast<uint4*>(buf)[i] = make_uint4(0, 0, 0, 0);
+  fence_async_smem();
+  __syncthreads();
+}
+
 // One launch of clusters of eight.  Cluster 0 sorts into pairs (passes of
 // kSortBits bits, ping-pong between buf0 and buf1, the last pass ending in
-// `pairs`); the others zero dE (n16 units of 16 bytes).  Each warp owns a
+// `pairs`), clears and fills the bitmap (null: none wanted) and clears the
+// count of crossing runs; the others zero the first zero_bytes of dE.  Each warp
+// owns a
 // contiguous part of the pairs: it counts its digits, the counts are scanned
 // over warps, CTAs (through distributed shared memory) and bins, and it places
 // its pairs, 32 at a time in order, ranked among equal digits by a match.
 __global__ void __cluster_dims__(kSortCluster, 1, 1) __launch_bounds__(kSortThreads)
     embed_sort_kernel(const int64_t* __restrict__ tokens, int M, int64_t V, int passes, int2* buf0, int2* buf1,
-                      uint4* dE, size_t n16) {
-  extern __shared__ uint32_t sm[];
+                      uint8_t* dE, size_t zero_bytes,
+                      uint32_t* bitmap, size_t words, int* crossing) {
+  extern __shared__ __align__(16) uint32_t sm[];
   pdl_begin();
   if (blockIdx.x >= kSortCluster) {
-    const size_t nthr = static_cast<size_t>(gridDim.x - kSortCluster) * kSortThreads;
-    for (size_t i = (blockIdx.x - kSortCluster) * static_cast<size_t>(kSortThreads) + threadIdx.x; i < n16; i += nthr)
-      dE[i] = make_uint4(0, 0, 0, 0);
+    zero_buffer(sm);
+    if (threadIdx.x == 0) {
+      constexpr size_t kTake = 8 * kZeroPiece;
+      for (size_t o = (blockIdx.x - kSortCluster) * kTake; o < zero_bytes; o += (gridDim.x - kSortCluster) * kTake)
+        zero_run(dE + o, zero_bytes - o < kTake ? zero_bytes - o : kTake, sm);
+      bulk_wait_all<0>();
+    }
     return;
   }
   uint32_t* hist = sm;                                      // [32 warps][bins]
@@ -132,6 +164,12 @@ __global__ void __cluster_dims__(kSortCluster, 1, 1) __launch_bounds__(kSortThre
   const int lo = static_cast<int>(lo64 < M ? lo64 : M);
   const int hi = static_cast<int>(lo64 + per < M ? lo64 + per : M);
   uint32_t* mine = hist + warp * kSortBins;
+  if (cta == 0 && threadIdx.x == 0) *crossing = 0;
+  if (bitmap != nullptr) {
+    for (size_t i = static_cast<size_t>(cta) * kSortThreads + threadIdx.x; i < words; i += kSortThreads * kSortCluster)
+      bitmap[i] = 0;
+    cluster_sync_all();
+  }
   for (int pass = 0; pass < passes; ++pass) {
     const int2* src = pass & 1 ? buf1 : buf0;
     int2* dst = pass & 1 ? buf0 : buf1;
@@ -147,7 +185,9 @@ __global__ void __cluster_dims__(kSortCluster, 1, 1) __launch_bounds__(kSortThre
       const bool on = i0 + lane < hi;
       const unsigned act = __ballot_sync(0xffffffffu, on);
       if (on) {
-        const uint32_t d = (static_cast<uint32_t>(get(i0 + lane).x) >> shift) & (kSortBins - 1);
+        const int tok = get(i0 + lane).x;
+        if (pass == 0 && bitmap != nullptr && tok < V) atomicOr(&bitmap[tok >> 5], 1u << (tok & 31));
+        const uint32_t d = (static_cast<uint32_t>(tok) >> shift) & (kSortBins - 1);
         const unsigned same = __match_any_sync(act, d);
         if ((same & ((1u << lane) - 1u)) == 0) mine[d] += __popc(same);
       }
@@ -215,53 +255,83 @@ __global__ void __cluster_dims__(kSortCluster, 1, 1) __launch_bounds__(kSortThre
   }
 }
 
-// Eight columns of dE[tok]: stored, or added to what is there.
-__device__ __forceinline__ void embed_put(float* dE, int64_t tok, int D, int c0, const float (&a)[8], float scale,
-                                          int accumulate) {
-  float4* o = reinterpret_cast<float4*>(dE + tok * D + c0);
-  float4 x = make_float4(scale * a[0], scale * a[1], scale * a[2], scale * a[3]);
-  float4 y = make_float4(scale * a[4], scale * a[5], scale * a[6], scale * a[7]);
-  if (accumulate) {
-    const float4 p = o[0], q = o[1];
-    x = make_float4(p.x + x.x, p.y + x.y, p.z + x.z, p.w + x.w);
-    y = make_float4(q.x + y.x, q.y + y.y, q.z + y.z, q.w + y.w);
+// Eight columns of dE[tok]: stored, or added to what is there (x, y); the
+// product is rounded by itself, so that what is added is what would be stored.
+__device__ __forceinline__ void embed_put(float4* o, const float (&a)[8], float scale, bool add, float4 x, float4 y) {
+  float s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = __fmul_rn(scale, a[e]);
+  if (add) {
+    s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
+    s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
   }
-  o[0] = x;
-  o[1] = y;
+  o[0] = make_float4(s[0], s[1], s[2], s[3]);
+  o[1] = make_float4(s[4], s[5], s[6], s[7]);
 }
 
 constexpr int kEmbBwdThreads = 256;  // 2048 columns, eight per thread
 constexpr int kEmbBwdMaxChunk = 1024;
 constexpr int kEmbBwdUnroll = 8;  // rows requested together
 
-// part: [items][2][D] -- a chunk's sum of the run that began before it, and of
-// the run that begins in it and goes on after it.
+// Blocks [0, items * spans) sum: chunk block / spans, columns from 2048 * (block
+// % spans).  part: [items][2][D] -- a chunk's sum of the run that began before
+// it, and of the run that begins in it and goes on after it; the chunks with the
+// latter are listed in `list` (in any order).  ACC: the sums are added to dE.
+// The other blocks each zero those of 2^unit rows (from zero_row on) that the
+// bitmap lacks.
+template <bool ACC>
 __global__ void __launch_bounds__(kEmbBwdThreads) embed_bwd_kernel(
     const int2* __restrict__ pairs, const __nv_bfloat16* __restrict__ dh, float scale, float* __restrict__ dE,
-    float* __restrict__ part, int M, int64_t V, int D, int chunk, int accumulate) {
-  __shared__ int2 sp[kEmbBwdMaxChunk];
-  __shared__ int edge[2];
+    float* __restrict__ part, int* __restrict__ list, int* __restrict__ crossing, int M, int64_t V, int D, int chunk,
+    int items, int spans, const uint32_t* __restrict__ bitmap, int64_t zero_row, int unit) {
+  __shared__ int2 sp[kEmbBwdMaxChunk + 1];
+  __shared__ int before;
   pdl_begin();
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * chunk;
-  const int n = static_cast<int>(M - p0 < chunk ? M - p0 : chunk);
-  for (int i = threadIdx.x; i < n; i += blockDim.x) sp[i] = pairs[p0 + i];
-  if (threadIdx.x == 0) {
-    edge[0] = p0 > 0 ? pairs[p0 - 1].x : -1;
-    edge[1] = p0 + n < M ? pairs[p0 + n].x : -1;
+  if (!ACC && blockIdx.x >= static_cast<unsigned>(items) * spans) {
+    const int64_t first = zero_row + (static_cast<int64_t>(blockIdx.x - items * spans) << unit);
+    const int rows = static_cast<int>(min(static_cast<int64_t>(1 << unit), V - first));  // all in one word
+    uint32_t free = ~(__ldg(bitmap + (first >> 5)) >> (first & 31)) & (rows == 32 ? ~0u : (1u << rows) - 1u);
+    while (free != 0) {
+      const int r0 = __ffs(free) - 1;
+      const uint32_t rest = ~(free >> r0);
+      const int n = rest == 0 ? 32 : __ffs(rest) - 1;  // free rows from r0 on
+      float4* o = reinterpret_cast<float4*>(dE + (first + r0) * D);
+      const size_t len = static_cast<size_t>(n) * D / 4;
+#pragma unroll 8
+      for (size_t i = threadIdx.x; i < len; i += blockDim.x) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      free = r0 + n >= 32 ? 0u : free & (~0u << (r0 + n));
+    }
+    return;
   }
+  const int item = static_cast<int>(blockIdx.x) / spans, span = static_cast<int>(blockIdx.x) % spans;
+  const int64_t p0 = static_cast<int64_t>(item) * chunk;
+  const int n = static_cast<int>(M - p0 < chunk ? M - p0 : chunk);
+  // (sp[n]: the pair after the chunk)
+  for (int i = threadIdx.x; i <= n; i += blockDim.x) sp[i] = p0 + i < M ? pairs[p0 + i] : make_int2(-1, 0);
+  if (threadIdx.x == 0) before = p0 > 0 ? pairs[p0 - 1].x : -1;
   __syncthreads();
-  const int c0 = (blockIdx.y * kEmbBwdThreads + threadIdx.x) * 8;
+  if (span == 0 && threadIdx.x == 0 && sp[n].x == sp[n - 1].x && sp[n].x < V && !(before == sp[n].x))
+    list[atomicAdd(crossing, 1)] = item;
+  const int c0 = (span * kEmbBwdThreads + threadIdx.x) * 8;
   if (c0 >= D) return;
   float a[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) a[e] = 0.f;
-  bool from_before = edge[0] == sp[0].x;
+  bool from_before = before == sp[0].x;
   for (int i0 = 0; i0 < n; i0 += kEmbBwdUnroll) {
     uint4 v[kEmbBwdUnroll];
+    float4 x[kEmbBwdUnroll], y[kEmbBwdUnroll];  // ACC: dE's row where a run ends
 #pragma unroll
-    for (int u = 0; u < kEmbBwdUnroll; ++u)
-      if (i0 + u < n && sp[i0 + u].x < V)
-        v[u] = __ldg(reinterpret_cast<const uint4*>(dh + static_cast<size_t>(sp[i0 + u].y) * D + c0));
+    for (int u = 0; u < kEmbBwdUnroll; ++u) {
+      const int i = i0 + u;
+      if (i >= n || sp[i].x >= V) continue;
+      v[u] = __ldcs(reinterpret_cast<const uint4*>(dh + static_cast<size_t>(sp[i].y) * D + c0));
+      if (ACC && sp[i + 1].x != sp[i].x) {
+        const float4* o = reinterpret_cast<const float4*>(dE + static_cast<size_t>(sp[i].x) * D + c0);
+        x[u] = __ldcs(o);
+        y[u] = __ldcs(o + 1);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kEmbBwdUnroll; ++u) {
       const int i = i0 + u;
@@ -273,15 +343,14 @@ __global__ void __launch_bounds__(kEmbBwdThreads) embed_bwd_kernel(
         a[2 * e] += bf16lo(w[e]);
         a[2 * e + 1] += bf16hi(w[e]);
       }
-      const int next = i + 1 < n ? sp[i + 1].x : edge[1];
-      const bool goes_on = i + 1 == n && next == tok;
-      if (next == tok && !goes_on) continue;
-      if (from_before || goes_on) {
-        float* o = part + (static_cast<size_t>(blockIdx.x) * 2 + (from_before ? 0 : 1)) * D + c0;
+      const bool ends = sp[i + 1].x != tok;
+      if (!ends && i + 1 < n) continue;
+      if (from_before || !ends) {
+        float* o = part + (static_cast<size_t>(item) * 2 + (from_before ? 0 : 1)) * D + c0;
         *reinterpret_cast<float4*>(o) = make_float4(a[0], a[1], a[2], a[3]);
         *reinterpret_cast<float4*>(o + 4) = make_float4(a[4], a[5], a[6], a[7]);
       } else {
-        embed_put(dE, tok, D, c0, a, scale, accumulate);
+        embed_put(reinterpret_cast<float4*>(dE + static_cast<size_t>(tok) * D + c0), a, scale, ACC, x[u], y[u]);
       }
       from_before = false;
 #pragma unroll
@@ -290,59 +359,63 @@ __global__ void __launch_bounds__(kEmbBwdThreads) embed_bwd_kernel(
   }
 }
 
-// The runs that cross a chunk's border: block (i, .) adds the parts of the run
-// that begins in chunk i and goes on after it.  Eight groups of 32 threads (256
-// columns) each add a contiguous share of the parts, in order; the groups' sums
-// are added in order.
+// The runs that cross a chunk's border: the listed chunk i and the parts of the
+// run that begins there and goes on after it.  A block takes 256 columns of one
+// run at a time.  Eight groups of 32 threads each add a contiguous share of the
+// parts, in order; the groups' sums are added in order.
 constexpr int kJoinGroups = 8;
 
 __global__ void __launch_bounds__(32 * kJoinGroups) embed_bwd_join_kernel(
-    const int2* __restrict__ pairs, const float* __restrict__ part, float scale, float* __restrict__ dE, int M,
-    int64_t V, int D, int chunk, int items, int accumulate) {
+    const int2* __restrict__ pairs, const float* __restrict__ part, const int* __restrict__ list,
+    const int* __restrict__ crossing, float scale, float* __restrict__ dE, int D, int chunk, int items,
+    int accumulate) {
   __shared__ float red[kJoinGroups][32][9];
   pdl_begin();
-  const int i = blockIdx.x;
-  const int64_t end = static_cast<int64_t>(i + 1) * chunk;  // the next chunk's first pair
-  if (end >= M) return;
-  const int tok = __ldg(&pairs[end - 1].x);
-  if (tok >= V || __ldg(&pairs[end].x) != tok) return;
-  const int64_t p0 = static_cast<int64_t>(i) * chunk;
-  if (p0 > 0 && __ldg(&pairs[p0 - 1].x) == tok) return;  // it began before this chunk
-  // chunks i + 1 .. i + n hold its other parts
-  int lo = i + 1, hi = items;  // first chunk in (i, items] whose first pair has another token
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(&pairs[static_cast<int64_t>(mid) * chunk].x) == tok)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  const int n = lo - i;  // parts: chunk i's second, then the first of chunks i + 1 .. lo - 1
+  const int spans = (D + 255) / 256;
+  const int64_t work = static_cast<int64_t>(__ldg(crossing)) * spans;
   const int grp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = (blockIdx.y * 32 + lane) * 8;
-  const int k0 = static_cast<int>(static_cast<int64_t>(n) * grp / kJoinGroups);
-  const int k1 = static_cast<int>(static_cast<int64_t>(n) * (grp + 1) / kJoinGroups);
-  float a[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) a[e] = 0.f;
-  if (c0 < D) {
-#pragma unroll 4
-    for (int k = k0; k < k1; ++k) {
-      const float* s = part + (static_cast<size_t>(i + k) * 2 + (k == 0 ? 1 : 0)) * D + c0;
-      const float4 x = *reinterpret_cast<const float4*>(s), y = *reinterpret_cast<const float4*>(s + 4);
-      a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
-      a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+  for (int64_t t = blockIdx.x; t < work; t += gridDim.x) {
+    const int i = __ldg(list + t / spans);
+    const int c0 = (static_cast<int>(t % spans) * 32 + lane) * 8;
+    const int tok = __ldg(&pairs[static_cast<int64_t>(i + 1) * chunk].x);
+    // its other parts are the first of chunks i + 1 .. lo - 1
+    int lo = i + 1, hi = items;  // first chunk in (i, items] whose first pair has another token
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(&pairs[static_cast<int64_t>(mid) * chunk].x) == tok)
+        lo = mid + 1;
+      else
+        hi = mid;
     }
-  }
+    const int n = lo - i;  // parts: chunk i's second, then those
+    const int k0 = static_cast<int>(static_cast<int64_t>(n) * grp / kJoinGroups);
+    const int k1 = static_cast<int>(static_cast<int64_t>(n) * (grp + 1) / kJoinGroups);
+    float a[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) red[grp][lane][e] = a[e];
-  __syncthreads();
-  if (grp == 0 && c0 < D) {
+    for (int e = 0; e < 8; ++e) a[e] = 0.f;
+    if (c0 < D) {
+#pragma unroll 4
+      for (int k = k0; k < k1; ++k) {
+        const float* s = part + (static_cast<size_t>(i + k) * 2 + (k == 0 ? 1 : 0)) * D + c0;
+        const float4 x = *reinterpret_cast<const float4*>(s), y = *reinterpret_cast<const float4*>(s + 4);
+        a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
+        a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+      }
+    }
 #pragma unroll
-    for (int g = 1; g < kJoinGroups; ++g)
+    for (int e = 0; e < 8; ++e) red[grp][lane][e] = a[e];
+    __syncthreads();
+    if (grp == 0 && c0 < D) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] += red[g][lane][e];
-    embed_put(dE, tok, D, c0, a, scale, accumulate);
+      for (int g = 1; g < kJoinGroups; ++g)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += red[g][lane][e];
+      float4* o = reinterpret_cast<float4*>(dE + static_cast<size_t>(tok) * D + c0);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (accumulate) x = o[0], y = o[1];
+      embed_put(o, a, scale, accumulate != 0, x, y);
+    }
+    __syncthreads();
   }
 }
 

@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(
 // A block walks rows blockIdx, + gridDim, ...; the next row's vectors are
 // requested before this row's sum is reduced (not with more than 512 threads,
 // whose 64 registers do not hold both rows).  dgamma's terms stay in registers
-// over the block's rows; part[block][N] is added up by dgamma_final_kernel in a
-// fixed order (the grid depends on the sizes alone).
+// over the block's rows; the blocks' sums part[block][N] are added up by
+// norm8_dgamma_kernel in a fixed order.
 template <int VPT, int MAXT>
 __global__ void __launch_bounds__(MAXT) add_rmsnorm_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ h, const float* __restrict__ r,
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_bwd_kernel(
   __shared__ float red[2][32];
   pdl_begin();
   if (threadIdx.x < 32) red[0][threadIdx.x] = red[1][threadIdx.x] = 0.f;
-  uint4 gv[VPT], yv[VPT], hv[VPT], sv[VPT];
+  uint4 yv[VPT], hv[VPT], sv[VPT];
   float dg[VPT][8];
   const auto load = [&](int64_t row) {
     const size_t ro = static_cast<size_t>(row) * N;
@@ -169,14 +169,15 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_bwd_kernel(
       }
     }
   };
+  const auto gamma_of = [&](int k) {  // (from L1: registers hold the rows in flight)
+    const int c = (threadIdx.x + k * blockDim.x) * 8;
+    return c < N ? __ldg(reinterpret_cast<const uint4*>(gamma + c)) : make_uint4(0, 0, 0, 0);
+  };
   if (kAhead) load(blockIdx.x);
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int c = (threadIdx.x + k * blockDim.x) * 8;
-    gv[k] = c < N ? __ldg(reinterpret_cast<const uint4*>(gamma + c)) : make_uint4(0, 0, 0, 0);
+  for (int k = 0; k < VPT; ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[k][e] = 0.f;
-  }
   if (blockDim.x > 32) __syncthreads();
   int it = 0;
   for (int64_t row = blockIdx.x; row < M; row += gridDim.x, it ^= 1) {
@@ -188,8 +189,9 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_bwd_kernel(
       y0[k] = yv[k];
       h0[k] = hv[k];
       s0[k] = sv[k];
+      const uint4 g = gamma_of(k);
       const uint32_t yw[4] = {y0[k].x, y0[k].y, y0[k].z, y0[k].w}, hw[4] = {h0[k].x, h0[k].y, h0[k].z, h0[k].w};
-      const uint32_t gw[4] = {gv[k].x, gv[k].y, gv[k].z, gv[k].w};
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         s = fmaf(bf16lo(yw[e]) * bf16lo(gw[e]), bf16lo(hw[e]), s);
@@ -203,8 +205,9 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_bwd_kernel(
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int c = (threadIdx.x + k * blockDim.x) * 8;
+      const uint4 g = gamma_of(k);
       const uint32_t yw[4] = {y0[k].x, y0[k].y, y0[k].z, y0[k].w}, hw[4] = {h0[k].x, h0[k].y, h0[k].z, h0[k].w};
-      const uint32_t sw[4] = {s0[k].x, s0[k].y, s0[k].z, s0[k].w}, gw[4] = {gv[k].x, gv[k].y, gv[k].z, gv[k].w};
+      const uint32_t sw[4] = {s0[k].x, s0[k].y, s0[k].z, s0[k].w}, gw[4] = {g.x, g.y, g.z, g.w};
       uint32_t o[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -226,6 +229,29 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_bwd_kernel(
       *reinterpret_cast<float4*>(o) = make_float4(dg[k][0], dg[k][1], dg[k][2], dg[k][3]);
       *reinterpret_cast<float4*>(o + 4) = make_float4(dg[k][4], dg[k][5], dg[k][6], dg[k][7]);
     }
+  }
+}
+
+// dgamma_j = sum over blocks of part[block][j]: a block takes 32 columns, warp w
+// the blocks w, w + 32, ..., whose sums are added in order.
+__global__ void __launch_bounds__(1024) norm8_dgamma_kernel(const float* __restrict__ part, int nblk, int N,
+                                                           float* __restrict__ dgamma) {
+  __shared__ float red[32][33];
+  pdl_begin();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (j < N) {
+#pragma unroll 8
+    for (int b = warp; b < nblk; b += 32) s += part[static_cast<size_t>(b) * N + j];
+  }
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && j < N) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) t += red[w][lane];
+    dgamma[j] = t;
   }
 }
 

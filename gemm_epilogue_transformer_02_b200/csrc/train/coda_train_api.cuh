@@ -34,49 +34,47 @@ coda_status_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t 
   return cudaLaunchKernelEx(&cfg, kern, KArgs(args)...) == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
 }
 
-// Sets a kernel's dynamic shared memory limit once per device.
-template <class K>
-coda_status_t set_smem(K kern, int bytes, int dev, bool (&done)[64]) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (done[dev]) return CODA_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return CODA_ERR_LAUNCH;
-  done[dev] = true;
-  return CODA_OK;
-}
-
 // ---------------------------------------------------------------- embedding
 
-// Pairs per block of the embedding backward: 32, so that a batch of some
-// thousand tokens gives a few hundred blocks; more once that would make over
+// Pairs per block of the embedding backward: 16, so that a batch of some
+// thousand tokens gives some hundred blocks; more once that would make over
 // 2048 blocks, which bounds the parts a run over many chunks is joined from.
 inline int embed_chunk(int64_t M) {
-  int64_t c = 32;
+  int64_t c = 16;
   while (c < coda::kEmbBwdMaxChunk && M > 2048 * c) c *= 2;
   return static_cast<int>(c);
 }
 
 struct EmbedWs {
-  size_t buf0, buf1, part, bytes;
+  size_t buf0, buf1, part, list, crossing, bitmap, words, bytes;
   int chunk, items;
 };
 
-inline EmbedWs embed_ws(int64_t M, int64_t D) {
+inline EmbedWs embed_ws(int64_t M, int64_t D, int64_t V) {
   EmbedWs w;
   w.chunk = embed_chunk(M);
   w.items = static_cast<int>((M + w.chunk - 1) / w.chunk);
+  w.words = static_cast<size_t>((V + 31) / 32);
   w.buf0 = 0;
   w.buf1 = align256(static_cast<size_t>(M) * 8);
   w.part = 2 * w.buf1;
-  w.bytes = w.part + align256(static_cast<size_t>(w.items) * 2 * D * 4);
+  w.list = w.part + align256(static_cast<size_t>(w.items) * 2 * D * 4);
+  w.crossing = w.list + align256(static_cast<size_t>(w.items) * 4);
+  w.bitmap = w.crossing + 256;
+  w.bytes = w.bitmap + align256(w.words * 4);
   return w;
 }
+
+// Bytes of dE that the sorting launch zeroes: as many as HBM takes while one
+// cluster sorts (14 us for 8192 tokens).
+inline size_t embed_zero_first(int64_t M) { return (size_t(48) << 20) + static_cast<size_t>(M) * 4096; }
 
 // --------------------------------------------------------------------- norm
 
 // A row's block: two 8-column vectors a thread (one for rows of up to 512), so
 // a row of up to 16384 columns stays in one block's registers.
 constexpr int64_t kNorm8MaxN = 16384;
+constexpr int kNorm8BwdThreads = 512;
 inline int norm8_vpt(int64_t N) { return N <= 512 ? 1 : 2; }
 inline int norm8_threads(int64_t N) {
   const int64_t t = (N / 8 + norm8_vpt(N) - 1) / norm8_vpt(N);
@@ -95,9 +93,10 @@ coda_status_t launch_norm8(const uint16_t* x, const uint16_t* res, const uint16_
                     q, sf, amax, r_out, M, static_cast<int>(N), static_cast<int>(nrb));
 }
 
-// Blocks of the norm's backward: 768 threads' worth for each of 148 SMs.
+// Blocks of the norm's backward: as many as 148 SMs hold at once (by registers,
+// about 512 threads an SM), so that every block has as many rows.
 inline int norm8_bwd_blocks(int64_t M, int64_t N) {
-  const int64_t b = std::max<int64_t>(1, 148 * 768 / norm8_threads(N));
+  const int64_t b = 148 * std::max<int64_t>(1, kNorm8BwdThreads / norm8_threads(N));
   return static_cast<int>(std::min<int64_t>(M, b));
 }
 
@@ -268,9 +267,9 @@ coda_status_t coda_embed(const int64_t* tokens, const uint16_t* E, float scale, 
                     static_cast<int>(nspan));
 }
 
-size_t coda_embed_bwd_workspace_size(int64_t M, int64_t D) {
-  if (M <= 0 || M > kMaxInt || !dim_ok(D)) return 0;
-  return embed_ws(M, D).bytes;
+size_t coda_embed_bwd_workspace_size(int64_t M, int64_t D, int64_t V) {
+  if (M <= 0 || M > kMaxInt || !dim_ok(D) || V <= 0 || V >= kMaxInt) return 0;
+  return embed_ws(M, D, V).bytes;
 }
 
 coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float scale, float* dE, int accumulate, void* ws,
@@ -278,7 +277,7 @@ coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float sc
   CODA_CHECK(M >= 0 && M <= kMaxInt && dim_ok(D) && V > 0 && V < kMaxInt, CODA_ERR_SHAPE);
   CODA_CHECK(dE && (M == 0 || (tokens && dh)), CODA_ERR_NULL);
   CODA_CHECK(al16(tokens) && al16(dh) && al16(dE) && al16(ws), CODA_ERR_ALIGN);
-  CODA_CHECK(M == 0 || (ws && ws_bytes >= embed_ws(M, D).bytes), CODA_ERR_WORKSPACE);
+  CODA_CHECK(M == 0 || (ws && ws_bytes >= embed_ws(M, D, V).bytes), CODA_ERR_WORKSPACE);
   if (M == 0 && accumulate) return CODA_OK;
   int dev;
   DevInfo* info;
@@ -288,9 +287,32 @@ coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float sc
   if (M == 0)
     return cudaMemsetAsync(dE, 0, static_cast<size_t>(V) * D * 4, s) == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
   static bool done[64];
-  st = set_smem(embed_sort_kernel, kSortSmem, dev, done);
-  if (st != CODA_OK) return st;
-  const EmbedWs w = embed_ws(M, D);
+  static int clusters[64];
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!done[dev]) {
+      if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem) !=
+          cudaSuccess)
+        return CODA_ERR_LAUNCH;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(kSortCluster * 64));
+      cfg.blockDim = dim3(kSortThreads);
+      cfg.dynamicSmemBytes = kSortSmem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = kSortCluster;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&clusters[dev], embed_sort_kernel, &cfg) != cudaSuccess || clusters[dev] < 2) {
+        cudaGetLastError();
+        clusters[dev] = 2;
+      }
+      done[dev] = true;
+    }
+  }
+  const EmbedWs w = embed_ws(M, D, V);
   uint8_t* base = static_cast<uint8_t*>(ws);
   int2* b0 = reinterpret_cast<int2*>(base + w.buf0);
   int2* b1 = reinterpret_cast<int2*>(base + w.buf1);
@@ -300,24 +322,39 @@ coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float sc
   const int passes = (bits + kSortBits - 1) / kSortBits;
   // pass 0 reads the tokens and writes b1, pass 1 writes b0, ...
   const int2* pairs = passes & 1 ? b1 : b0;
-  const size_t n16 = accumulate ? 0 : static_cast<size_t>(V) * D / 4;
-  // zeroing: enough clusters that each thread stores 64 bytes or more, at most
-  // one 1024-thread CTA per SM beside the sorting ones
-  const int64_t zc = std::min<int64_t>(info->sms / kSortCluster,
-                                       static_cast<int64_t>((n16 + 4 * kSortThreads * kSortCluster - 1) /
-                                                            (4 * kSortThreads * kSortCluster)));
+  int* list = reinterpret_cast<int*>(base + w.list);
+  int* crossing = reinterpret_cast<int*>(base + w.crossing);
+  uint32_t* bitmap = accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + w.bitmap);
+  const size_t row = static_cast<size_t>(D) * 4;
+  // whole words of the bitmap (32 rows) go to the sorting launch
+  const int64_t zero_row =
+      accumulate ? 0 : std::min<int64_t>(V, static_cast<int64_t>(embed_zero_first(M) / (32 * row)) * 32);
+  // a cluster for every eight takes of eight pieces, at most as many as run at
+  // once beside the sorting one (a second wave of them took 120 us more)
+  const size_t take = size_t(64) * kZeroPiece;
+  const int64_t zc = std::min<int64_t>(clusters[dev] - 1, static_cast<int64_t>((zero_row * row + take - 1) / take));
   st = launch_pdl(embed_sort_kernel, dim3(static_cast<unsigned>(kSortCluster * (1 + zc))), kSortThreads, kSortSmem, 0,
-                  s, tokens, static_cast<int>(M), V, passes, b0, b1, reinterpret_cast<uint4*>(dE), n16);
+                  s, tokens, static_cast<int>(M), V, passes, b0, b1, reinterpret_cast<uint8_t*>(dE), zero_row * row,
+                  bitmap, w.words, crossing);
   if (st != CODA_OK) return st;
   const int threads = static_cast<int>(std::min<int64_t>(kEmbBwdThreads, (D / 8 + 31) & ~int64_t(31)));
-  st = launch_pdl(embed_bwd_kernel,
-                  dim3(static_cast<unsigned>(w.items), static_cast<unsigned>((D + 8 * kEmbBwdThreads - 1) / (8 * kEmbBwdThreads))),
-                  threads, 0, 0, s, pairs, reinterpret_cast<const __nv_bfloat16*>(dh), scale, dE, part,
-                  static_cast<int>(M), V, static_cast<int>(D), w.chunk, accumulate ? 1 : 0);
+  const int spans = static_cast<int>((D + 8 * kEmbBwdThreads - 1) / (8 * kEmbBwdThreads));
+  CODA_CHECK(static_cast<int64_t>(w.items) * spans < kMaxInt / 2, CODA_ERR_SHAPE);
+  // a zeroing block takes about 64 KB of rows, so that the blocks that run
+  // together write a compact range
+  int unit = 0;
+  while (unit < 5 && (row << (unit + 1)) <= 65536) ++unit;
+  const int64_t zb = accumulate ? 0 : (V - zero_row + (1 << unit) - 1) >> unit;
+  CODA_CHECK(zb < kMaxInt / 2, CODA_ERR_SHAPE);
+  auto sum = accumulate ? embed_bwd_kernel<true> : embed_bwd_kernel<false>;
+  st = launch_pdl(sum, dim3(static_cast<unsigned>(w.items * spans + zb)), threads, 0, 0, s, pairs,
+                  reinterpret_cast<const __nv_bfloat16*>(dh), scale, dE, part, list, crossing, static_cast<int>(M), V,
+                  static_cast<int>(D), w.chunk, w.items, spans, static_cast<const uint32_t*>(bitmap), zero_row, unit);
   if (st != CODA_OK || w.items == 1) return st;
-  return launch_pdl(embed_bwd_join_kernel, dim3(static_cast<unsigned>(w.items - 1), static_cast<unsigned>((D + 255) / 256)),
-                    32 * kJoinGroups, 0, 0, s, pairs, static_cast<const float*>(part), scale, dE, static_cast<int>(M), V,
-                    static_cast<int>(D), w.chunk, w.items, accumulate ? 1 : 0);
+  const int64_t jb = std::min<int64_t>(2 * info->sms, (w.items - 1) * ((D + 255) / 256));
+  return launch_pdl(embed_bwd_join_kernel, dim3(static_cast<unsigned>(jb)), 32 * kJoinGroups, 0, 0, s, pairs,
+                    static_cast<const float*>(part), static_cast<const int*>(list), static_cast<const int*>(crossing),
+                    scale, dE, static_cast<int>(D), w.chunk, w.items, accumulate ? 1 : 0);
 }
 
 coda_status_t coda_add_rmsnorm_mx(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float eps,
@@ -386,9 +423,8 @@ coda_status_t coda_add_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const 
                   reinterpret_cast<const __nv_bfloat16*>(gamma), reinterpret_cast<const __nv_bfloat16*>(d_h),
                   reinterpret_cast<__nv_bfloat16*>(dx_out), static_cast<float*>(ws), M, static_cast<int>(N));
   if (st != CODA_OK) return st;
-  dgamma_final_kernel<<<static_cast<unsigned>((N + kDgCols - 1) / kDgCols), kDgCols * kDgGroups, 0, s>>>(
-      static_cast<const float*>(ws), blocks, static_cast<int>(N), dgamma_out);
-  return cudaGetLastError() == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
+  return launch_pdl(norm8_dgamma_kernel, dim3(static_cast<unsigned>((N + 31) / 32)), 1024, 0, 0, s,
+                    static_cast<const float*>(ws), blocks, static_cast<int>(N), dgamma_out);
 }
 
 size_t coda_newton_schulz_workspace_size(int64_t batch, int64_t m, int64_t n) {

@@ -505,9 +505,10 @@ coda_status_t coda_gemm_rowscale_partial_mx(const uint8_t* Aq, const uint8_t* As
 coda_status_t coda_embed(const int64_t* tokens, const uint16_t* E, float scale, const uint16_t* gamma, uint16_t* h_out,
                          uint16_t* hg_out, float* partial, int64_t M, int64_t D, int64_t V, void* stream);
 
-/* Bytes of workspace coda_embed_bwd needs (0 for M <= 0): the sorted (token,
- * row) pairs and the sums of runs that cross a block's border. */
-size_t coda_embed_bwd_workspace_size(int64_t M, int64_t D);
+/* Bytes of workspace coda_embed_bwd needs (0 for M <= 0 or a bad shape): the
+ * sorted (token, row) pairs, the sums of runs that cross a block's border and a
+ * bit per token. */
+size_t coda_embed_bwd_workspace_size(int64_t M, int64_t D, int64_t V);
 
 /* Gradient of coda_embed's h: dE[v] = scale * sum over i with tokens[i] = v of
  * dh_i, in fp32 with increasing i within blocks of fixed size (the same bits

@@ -113,13 +113,13 @@ def tokens_of(kind, M, V, g):
 
 @pytest.mark.parametrize("kind", ["uniform", "one", "padding", "runs", "half"])
 @pytest.mark.parametrize("M,D,V", [(1, 8, 1), (31, 16, 3), (33, 264, 40), (1000, 2056, 97), (4097, 64, 5000),
-                                   (300, 8, 300000)])
+                                   (300, 8, 300000), (700, 512, 30011)])
 def test_embed_bwd(kind, M, D, V):
     g = gen(M * 3 + D)
     tokens = tokens_of(kind, M, V, g)
     dh = randn(g, M, D).to(BF)
     dE = Guarded((V, D), F32)
-    ws = Guarded((C.load_library().coda_embed_bwd_workspace_size(M, D),), U8)
+    ws = Guarded((C.load_library().coda_embed_bwd_workspace_size(M, D, V),), U8)
     C.embed_bwd(tokens, dh, V, 3.0, dE_out=dE.t, ws=ws.t)
     assert dE.intact() and ws.intact()
     ref, mag = embed_bwd_ref(tokens, dh, V, 3.0)

@@ -42,9 +42,10 @@ def test_embed_refusals(lib):
 @no_gpu_only
 def test_embed_bwd_refusals(lib):
     f, size = lib.coda_embed_bwd, lib.coda_embed_bwd_workspace_size
-    n = size(4, 64)
+    n = size(4, 64, 10)
     assert n >= 2 * 4 * 8 + 2 * 64 * 4
-    assert size(0, 64) == 0 and size(4, 60) == 0 and size(-1, 64) == 0
+    assert size(4, 64, 1 << 20) >= (1 << 20) // 8
+    assert size(0, 64, 10) == 0 and size(4, 60, 10) == 0 and size(-1, 64, 10) == 0 and size(4, 64, 0) == 0
     assert f(P, Q, 1.0, R, 0, S, n - 1, 4, 64, 10, None) == WS
     assert f(P, Q, 1.0, R, 0, None, n, 4, 64, 10, None) == WS
     assert f(P, Q, 1.0, R, 1, None, 0, 0, 64, 10, None) == OK    # an empty batch adds nothing
