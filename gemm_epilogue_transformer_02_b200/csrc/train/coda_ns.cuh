@@ -685,15 +685,20 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
       for (NsSeq s(p); ok && s.next(p);) {
         const int nunits = ns_units(p, s);
+        // the first unit and its operands are worked out before the barrier
+        NsUnit n = ns_unit(p, s, first);
+        NsOperand op[2];
+        ns_operands(p, s, n.job, op[0], op[1]);
         if (s.ph > 0) {
           if (!ns_count_wait(p.counters, arrivals * s.ph, w)) break;
           fence_proxy_async_global();  // the loads below see what other CTAs' copies wrote
           mbar_arrive(go);
         }
         for (int u = first; ok && u < nunits; u += step) {
-          const NsUnit n = ns_unit(p, s, u);
-          NsOperand op[2];
-          ns_operands(p, s, n.job, op[0], op[1]);
+          if (u != first) {
+            n = ns_unit(p, s, u);
+            ns_operands(p, s, n.job, op[0], op[1]);
+          }
           for (int kb = n.kb0; kb < n.kb1; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
               ok = false;
@@ -828,11 +833,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       const int nunits = ns_units(p, s);
       const int gen = static_cast<int>(gens >> (16 * s.geo())) & 0xffff;
       gens += 1ull << (16 * s.geo());
+      NsUnit n = ns_unit(p, s, first);
       // (also without a unit: an arrival must not come before the previous barrier)
       if (s.ph > 0 && !__all_sync(0xffffffffu, mbar_wait(go, (s.ph - 1) & 1, w))) break;
       if (lane == 0) fence_proxy_async_global();
       for (int u = first; ok && u < nunits; u += step, ++it) {
-        const NsUnit n = ns_unit(p, s, u);
+        if (u != first) n = ns_unit(p, s, u);
         const int acc = it & 1;
         const uint32_t par = (it >> 1) & 1;
         if (s.f.kind == kNsSquare)
