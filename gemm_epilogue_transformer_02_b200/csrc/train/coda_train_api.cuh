@@ -74,7 +74,6 @@ inline size_t embed_zero_first(int64_t M) { return (size_t(48) << 20) + static_c
 // A row's block: two 8-column vectors a thread (one for rows of up to 512), so
 // a row of up to 16384 columns stays in one block's registers.
 constexpr int64_t kNorm8MaxN = 16384;
-constexpr int kNorm8BwdThreads = 512;
 inline int norm8_vpt(int64_t N) { return N <= 512 ? 1 : 2; }
 inline int norm8_threads(int64_t N) {
   const int64_t t = (N / 8 + norm8_vpt(N) - 1) / norm8_vpt(N);
@@ -93,11 +92,12 @@ coda_status_t launch_norm8(const uint16_t* x, const uint16_t* res, const uint16_
                     q, sf, amax, r_out, M, static_cast<int>(N), static_cast<int>(nrb));
 }
 
-// Blocks of the norm's backward: as many as 148 SMs hold at once (by registers,
-// about 512 threads an SM), so that every block has as many rows.
+// Blocks of the norm's backward: as many as 148 SMs hold at once, so that every
+// block has as many rows.
 inline int norm8_bwd_blocks(int64_t M, int64_t N) {
-  const int64_t b = 148 * std::max<int64_t>(1, kNorm8BwdThreads / norm8_threads(N));
-  return static_cast<int>(std::min<int64_t>(M, b));
+  const int t = norm8_threads(N);
+  const int64_t per_sm = t <= 64 ? 640 / t : (t <= 128 ? 5 : (t <= 256 ? 2 : 1));
+  return static_cast<int>(std::min<int64_t>(M, 148 * per_sm));
 }
 
 // ------------------------------------------------------------ Newton-Schulz
@@ -416,8 +416,11 @@ coda_status_t coda_add_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const 
     return cudaMemsetAsync(dgamma_out, 0, static_cast<size_t>(N) * 4, s) == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
   const int blocks = norm8_bwd_blocks(M, N);
   const int threads = norm8_threads(N);
-  auto kern = norm8_vpt(N) == 1 ? add_rmsnorm_bwd_kernel<1, 64>
-                                : (threads <= 512 ? add_rmsnorm_bwd_kernel<2, 512> : add_rmsnorm_bwd_kernel<2, 1024>);
+  auto kern = norm8_vpt(N) == 1 ? add_rmsnorm_bwd_kernel<1, 64, 10>
+                                : (threads <= 128   ? add_rmsnorm_bwd_kernel<2, 128, 5>
+                                   : threads <= 256 ? add_rmsnorm_bwd_kernel<2, 256, 2>
+                                   : threads <= 512 ? add_rmsnorm_bwd_kernel<2, 512, 1>
+                                                    : add_rmsnorm_bwd_kernel<2, 1024, 1>);
   st = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), threads, 0, 0, s,
                   reinterpret_cast<const __nv_bfloat16*>(dy), reinterpret_cast<const __nv_bfloat16*>(h), r,
                   reinterpret_cast<const __nv_bfloat16*>(gamma), reinterpret_cast<const __nv_bfloat16*>(d_h),
