@@ -63,14 +63,32 @@ constexpr float kNsScaleP = 256.f;   // P, Q
 
 constexpr int kNsEpiWarps = 8;                     // two per TMEM lane quarter, each half of a tile's columns
 constexpr int kNsThreads = 64 + 32 * kNsEpiWarps;  // TMA producer, MMA issuer, epilogue warps
-constexpr int kNsStages = 5;
-constexpr int kNsOpBytes = 128 * 64 * 2;  // one operand's 128 rows of a 64-wide k-block
-constexpr int kNsStageBytes = 2 * kNsOpBytes;
-constexpr int kNsBoxBytes = 32 * 32 * 2;      // a 32 x 32 box of an epilogue
-constexpr int kNsEpiBytes = 4 * kNsBoxBytes;  // per epilogue warp: two buffers of a high and a low box
-constexpr int kNsBars = 2 * kNsStages + 2 + 2 + 1 + 1 + 2 * kNsEpiWarps;
-constexpr int kNsSmemBytes = 1024 + kNsStages * kNsStageBytes + kNsEpiWarps * kNsEpiBytes + kNsBars * 8 + 32;
-static_assert(kNsSmemBytes <= 232448, "shared memory");
+constexpr int kNsBoxBytes = 32 * 32 * 2;  // a 32 x 32 box of an epilogue
+
+// A tile's shape and what a CTA keeps for it in shared memory.  N = 256: a
+// cluster of two CTAs per 256 x 256 tile (cta_group::2; rank r owns accumulator
+// rows [128 r, 128 r + 128) and loads those rows of the left operand and its
+// half of the right one's).  N = 128, 64: one CTA per 128 x N tile.  A 128 x 64
+// tile gives each epilogue warp one block, and eight stages hold a K of 512 at
+// once; it is for matrices whose tiles would leave most SMs idle.
+template <int N>
+struct NsTile {
+  static constexpr bool kPair = N == 256;
+  static constexpr int kM = kPair ? 256 : 128;
+  static constexpr int kN = N;
+  static constexpr int kStages = N == 64 ? 8 : 5;
+  static constexpr int kRight = kPair ? 128 : N;                       // rows of the right operand a CTA loads
+  static constexpr int kLeftBytes = 128 * 64 * 2;                      // of a 64-wide k-block
+  static constexpr int kStageBytes = kLeftBytes + kRight * 64 * 2;
+  static constexpr int kHalf = N / 2;                                  // columns of an epilogue warp
+  static constexpr int kBlks = kHalf / 32;                             // blocks of 32 columns
+  static constexpr int kBufs = kBlks > 1 ? 2 : 1;                      // its staging buffers: a high and a low box
+  static constexpr int kEpiBytes = kBufs * 2 * kNsBoxBytes;
+  static constexpr int kWarps = (kPair ? 2 : 1) * kNsEpiWarps;         // epilogue warps of a tile
+  static constexpr int kBars = 2 * kStages + 2 + 2 + 1 + 1 + 2 * kNsEpiWarps;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kNsEpiWarps * kEpiBytes + kBars * 8 + 32;
+  static_assert(kSmem <= 232448, "shared memory");
+};
 
 enum NsKind : int { kNsGram = 0, kNsSquare, kNsMul, kNsUpdate };
 
@@ -88,10 +106,18 @@ enum NsGeoIndex : int { kGeoGram = 0, kGeoSym, kGeoSym2, kGeoUpdate, kGeos };
 // The symmetric matrices: A, P, P A, and the group's product Q (two, in turn).
 enum NsBuf : int { kBufA = 0, kBufP, kBufT, kBufQ0, kBufQ1, kBufs };
 
+// The loads of one matrix [batch, y, x], with 64-wide k-blocks.  A K-major
+// operand's 128 rows come as one copy: a single thread issues them, and at the
+// start of a GEMM the first MMAs wait for that (as two copies 5 to 7 % more time;
+// an MN-major operand's 128 rows as one 4-D copy took longer than as two).
+struct NsMaps {
+  CUtensorMap k128;  // K-major: 128 rows (y) x 64 k (x)
+  CUtensorMap b64;   // 64 x 64, of either form
+};
+
 struct NsParams {
-  // loads, 3-D [batch, y, x] with 64-wide boxes: 128 rows (K-major operand) or 64 k (MN-major)
-  CUtensorMap Xk[2], Xmn[2];  // X's high part, by group parity
-  CUtensorMap Sk[kBufs], Smn[kBufs];
+  NsMaps X[2];  // X's high part, by group parity
+  NsMaps S[kBufs];
   // the epilogues' boxes of 32 x 32 (64-byte swizzle): X's high and low parts, the symmetric matrices, the output
   CUtensorMap Hbox[2], Lbox[2], Sbox[kBufs], Obox;
   float2* diag[kBufs];  // [batch, s]: (d, f): what fp16 drops of the diagonal, and the rounded diagonal
@@ -154,23 +180,22 @@ struct NsSeq {
   }
 };
 
-// 3-D tiled copies (x, y, batch).
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1,
+// 3-D tiled copies (x, y, batch).  PAIR: the barrier may be the other CTA's.
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
                                             int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-      "[%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* m, uint32_t bar_cluster_addr,
-                                                 int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
-      "%5}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
+  if (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5}], [%2];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
 }
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* smem_src, int c0, int c1, int c2) {
@@ -261,10 +286,10 @@ struct NsUnit {
   int split;  // the split tile's number
 };
 
-// A symmetric result takes the tiles on and below the diagonal, row by row: row
-// i starts at tile i (i + 1) / 2.  Otherwise the tiles that share the longer
+// A symmetric result takes the square blocks on and below the diagonal, row by
+// row (row i starts at block i (i + 1) / 2), each of kM / kN tiles.  Otherwise the tiles that share the longer
 // side's operand follow each other.
-template <bool SYM>
+template <bool SYM, class T>
 __device__ __forceinline__ NsUnit ns_unit_of(const NsGeo& g, int batch, int u) {
   NsUnit n;
   int t = u;
@@ -287,11 +312,14 @@ __device__ __forceinline__ NsUnit ns_unit_of(const NsGeo& g, int batch, int u) {
   n.job = n.bz >= batch ? 1 : 0;
   n.bz -= n.job * batch;
   if (SYM) {
+    constexpr int kParts = T::kM / T::kN;
+    const int part = t % kParts;
+    t /= kParts;
     int i = static_cast<int>((sqrtf(8.f * static_cast<float>(t) + 1.f) - 1.f) * 0.5f);
     while (i * (i + 1) / 2 > t) --i;
     while ((i + 1) * (i + 2) / 2 <= t) ++i;
     n.rt = i;
-    n.ct = t - i * (i + 1) / 2;
+    n.ct = (t - i * (i + 1) / 2) * kParts + part;
   } else if (g.n_rt <= g.n_ct) {
     n.ct = t / g.n_rt;
     n.rt = t - n.ct * g.n_rt;
@@ -302,9 +330,10 @@ __device__ __forceinline__ NsUnit ns_unit_of(const NsGeo& g, int batch, int u) {
   return n;
 }
 
+template <class T>
 __device__ __forceinline__ NsUnit ns_unit(const NsParams& p, const NsSeq& s, int u) {
   const int g = s.geo();
-  return g == kGeoUpdate ? ns_unit_of<false>(p.geo[g], p.batch, u) : ns_unit_of<true>(p.geo[g], p.batch, u);
+  return g == kGeoUpdate ? ns_unit_of<false, T>(p.geo[g], p.batch, u) : ns_unit_of<true, T>(p.geo[g], p.batch, u);
 }
 
 __device__ __forceinline__ int ns_units(const NsParams& p, const NsSeq& s) {
@@ -312,26 +341,45 @@ __device__ __forceinline__ int ns_units(const NsParams& p, const NsSeq& s) {
   return g.whole + g.rest * g.splits;
 }
 
-// An operand of one GEMM: its two views, and whether the k-block kb of the rows
-// of tile `t` is loaded [k, row] (the MN-major view).
+// An operand of one GEMM.  Of a symmetric matrix the blocks of M x M on and below
+// the diagonal are stored: of a tile's rows (the first is `row`) the k-blocks
+// from first_mn on lie above it and are loaded [k, row] (MN-major).
+enum NsMajor : int { kNsK = 0, kNsMN, kNsSym };
 struct NsOperand {
-  const CUtensorMap *k, *mn;
-  int sym;  // blocks of the tile's size on and below the diagonal are stored
-  __device__ __forceinline__ bool is_mn(int t, int kb, int tile) const { return sym ? kb * 64 / tile > t : mn != nullptr; }
+  const NsMaps* maps;
+  int major;
+  template <int M>
+  __device__ __forceinline__ int first_mn(int row) const {
+    return major == kNsMN ? 0 : (major == kNsK ? 1 << 30 : (row / M + 1) * (M / 64));
+  }
 };
 
 __device__ __forceinline__ void ns_operands(const NsParams& p, const NsSeq& s, int job, NsOperand& P, NsOperand& Q) {
-  const int par = s.group & 1;
   const int l = job ? s.f.l2 : s.f.l, r = job ? s.f.r2 : s.f.r;
-  const NsOperand xk{&p.Xk[par], nullptr, 0}, xm{nullptr, &p.Xmn[par], 0}, sl{&p.Sk[l], &p.Smn[l], 1};
+  const NsMaps* x = &p.X[s.group & 1];
   if (s.f.kind == kNsGram) {
-    P = Q = p.tall ? xm : xk;
+    P = Q = NsOperand{x, p.tall ? kNsMN : kNsK};
   } else if (s.f.kind == kNsUpdate) {
-    P = p.tall ? xk : sl;
-    Q = p.tall ? sl : xm;
+    const NsOperand sl{&p.S[l], kNsSym};
+    P = p.tall ? NsOperand{x, kNsK} : sl;
+    Q = p.tall ? sl : NsOperand{x, kNsMN};
   } else {
-    P = sl;
-    Q = NsOperand{&p.Sk[r], &p.Smn[r], 1};
+    P = NsOperand{&p.S[l], kNsSym};
+    Q = NsOperand{&p.S[r], kNsSym};
+  }
+}
+
+// An operand's `ROWS` rows at r0 of one k-block, to shared memory (addresses as
+// the instruction takes them: the loop that issues these is as long as a
+// k-block's MMAs on small tiles).
+template <int ROWS, bool PAIR>
+__device__ __forceinline__ void ns_load(uint32_t dst, const NsMaps* maps, bool mn, int r0, int k0, int bz,
+                                        uint32_t bar) {
+  if (!mn) {
+    tma_load_3d<PAIR>(dst, ROWS == 128 ? &maps->k128 : &maps->b64, bar, k0, r0, bz);
+  } else {
+#pragma unroll
+    for (int j = 0; j < ROWS / 64; ++j) tma_load_3d<PAIR>(dst + j * 8192, &maps->b64, bar, r0 + j * 64, k0, bz);
   }
 }
 
@@ -371,12 +419,11 @@ __device__ __forceinline__ void ns_add4(uint32_t (&v)[32], int j, const float4& 
 // columns each, or tensor-memory loads of 8 columns in a small loop, were
 // slower.  Returns false if a wait gave up.
 // KIND kNsGram: gram or product (a product has a correction on the diagonal).
-template <int KIND, bool PAIR>
+template <int KIND, class T>
 __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, const NsUnit& n, int gen, int acc,
                                             uint32_t parity, uint64_t* tfull, NsEpi& e, const WaitCtx& w) {
-  constexpr int kTile = PAIR ? 256 : 128;
-  constexpr int kHalf = kTile / 2;  // columns of this warp
-  constexpr int kBlks = kHalf / 32;
+  constexpr int kHalf = T::kHalf;
+  constexpr int kBlks = T::kBlks;
   const int gi = s.geo();
   const NsGeo& g = p.geo[gi];
   const int buf_l = n.job ? s.f.l2 : s.f.l, buf_r = n.job ? s.f.r2 : s.f.r, buf_out = n.job ? s.f.out2 : s.f.out;
@@ -387,9 +434,9 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
   const CUtensorMap* in0 = KIND == kNsSquare ? &p.Sbox[kBufA] : &p.Hbox[par];
   const CUtensorMap* in1 = &p.Lbox[par];
   const int lane = e.lane;
-  const int row0 = n.rt * kTile + e.rank * 128 + e.q * 32;
+  const int row0 = n.rt * T::kM + e.rank * 128 + e.q * 32;
   const int row = row0 + lane;
-  const int col0 = n.ct * kTile + e.half * kHalf;
+  const int col0 = n.ct * T::kN + e.half * kHalf;
   const bool live = row < g.rows;
   // The diagonal of P: of the row of P X, of the column of X P.  Written by
   // other CTAs of this launch: read through L2.
@@ -405,7 +452,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
   if (row0 >= g.rows || nblk < 0) nblk = 0;  // (uniform over the warp)
   // the blocks this warp finishes: all, or of a split tile this part's share
   int b0 = 0, b1 = nblk;
-  if (n.part >= 0) {
+  if (kBlks > 1 && n.part >= 0) {
     b0 = n.part * (kBlks / g.splits);
     b1 = min(nblk, b0 + kBlks / g.splits);
   }
@@ -415,10 +462,11 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
     const int c = col0 + b * 32;
     if (lane == 0) {
       bulk_wait_read<0>();  // the buffer's last store has left it
-      uint8_t* d = e.stg + (cnt & 1) * (2 * kNsBoxBytes);
-      mbar_arrive_expect_tx(&e.bars[cnt & 1], in_low ? 2 * kNsBoxBytes : kNsBoxBytes);
-      tma_load_3d(d, in0, &e.bars[cnt & 1], c, row0, n.bz);
-      if (in_low) tma_load_3d(d + kNsBoxBytes, in1, &e.bars[cnt & 1], c, row0, n.bz);
+      uint8_t* d = e.stg + (cnt & (T::kBufs - 1)) * (2 * kNsBoxBytes);
+      mbar_arrive_expect_tx(&e.bars[cnt & (T::kBufs - 1)], in_low ? 2 * kNsBoxBytes : kNsBoxBytes);
+      tma_load_3d<false>(smem_u32(d), in0, smem_u32(&e.bars[cnt & (T::kBufs - 1)]), c, row0, n.bz);
+      if (in_low) 
+        tma_load_3d<false>(smem_u32(d + kNsBoxBytes), in1, smem_u32(&e.bars[cnt & (T::kBufs - 1)]), c, row0, n.bz);
     }
     if (by_col && c + lane < g.cols) {
       dc = __ldcg(dv + c + lane);
@@ -429,15 +477,15 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
   // Warp-uniform outcomes: tcgen05.ld below is a warp-collective instruction.
   if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], parity, w))) return false;
   tc_fence_after();
-  const uint32_t taddr = e.taddr + acc * kTile + e.half * kHalf;
+  const uint32_t taddr = e.taddr + acc * T::kN + e.half * kHalf;
   // A split tile: each part hands the others' blocks of its accumulator over
   // through memory, waits for theirs and adds up the parts of its own blocks in
   // an order that does not depend on whose they are.  The parts run at the same
   // time (they are the last units of their CTAs in this GEMM).  A lane's float4
   // lie 512 bytes apart, so a warp's access is contiguous.
-  constexpr size_t kPart = static_cast<size_t>(PAIR ? 16 : 8) * 32 * kHalf / 4;  // float4 of a tile's part
+  constexpr size_t kPart = static_cast<size_t>(T::kWarps) * 32 * kHalf / 4;  // float4 of a tile's part
   float4* part = nullptr;
-  if (n.part >= 0 && nblk > 0) {
+  if (kBlks > 1 && n.part >= 0 && nblk > 0) {
     const int region = (e.rank * 4 + e.q) * 2 + e.half;
     part = reinterpret_cast<float4*>(p.part) + static_cast<size_t>(n.split) * g.splits * kPart +
            region * (32 * kHalf / 4) + lane;
@@ -456,7 +504,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
     __syncwarp();
     int ok = 1;
     if (lane == 0) {
-      int* c = p.counters + 1 + gi * kNsSplitCounters + n.split * (PAIR ? 16 : 8) + region;
+      int* c = p.counters + 1 + gi * kNsSplitCounters + n.split * T::kWarps + region;
       red_release_add(c, 1);
       if (b0 < b1) ok = ns_count_wait(c, g.splits * (gen + 1), w) ? 1 : 0;
     }
@@ -471,12 +519,12 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
 #pragma unroll 1
   for (int b = b0; b < b1; ++b, ++e.cnt) {
     const int c32 = col0 + b * 32;
-    const int buf = e.cnt & 1;
+    const int buf = e.cnt & (T::kBufs - 1);
     uint8_t* S0 = e.stg + buf * (2 * kNsBoxBytes);
     uint8_t* S1 = S0 + kNsBoxBytes;
     const float2 dcb = dc;
     if (KIND == kNsGram) {
-      if (lane == 0) bulk_wait_read<1>();
+      if (lane == 0) bulk_wait_read<T::kBufs - 1>();
       __syncwarp();
     } else {
       if (b + 1 < b1) fetch(b + 1, e.cnt + 1);
@@ -492,7 +540,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
     uint32_t v[32];
     tmem_ld32(taddr + b * 32, v);
     tmem_ld_wait(v);
-    if (part != nullptr) {
+    if (kBlks > 1 && part != nullptr) {
       // (p0 + p1), or (p0 + p1) + (p2 + p3): own and partner first, then the other pair
       const float4* f = part + b * 256;
       float4 o[8], q[8];
@@ -616,19 +664,16 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
 // completed; its producer thread polls the counter, loads on, and lets the
 // epilogue warps go on through an mbarrier.  All CTAs have to be resident at
 // once, so the launch is a cooperative one.
-//
-// PAIR: a cluster of two CTAs per 256 x 256 tile (cta_group::2, rank r owns
-// accumulator rows [128 r, 128 r + 128) and loads those rows of P and its half
-// of Q's); otherwise one CTA per 128 x 128 tile.
-template <bool PAIR>
+template <class T>
 __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant__ NsParams p) {
-  constexpr int kTile = PAIR ? 256 : 128;
+  constexpr bool PAIR = T::kPair;
+  constexpr int kStages = T::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sEpi = smem + kNsStages * kNsStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + kNsEpiWarps * kNsEpiBytes);
-  uint64_t* empty = full + kNsStages;
-  uint64_t* tfull = empty + kNsStages;
+  uint8_t* sEpi = smem + kStages * T::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + kNsEpiWarps * T::kEpiBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint64_t* go = drain + 1;  // the grid barrier after each GEMM, for this CTA's epilogue warps
@@ -645,7 +690,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   const int arrivals = static_cast<int>(gridDim.x);  // per phase
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kNsStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -662,10 +707,10 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   }
   if (warp == 1) {
     if (PAIR) {
-      tmem_alloc_pair(tmem_holder, 2 * kTile);
+      tmem_alloc_pair(tmem_holder, 2 * T::kN);
       tmem_relinquish_pair();
     } else {
-      tmem_alloc(tmem_holder, 2 * kTile);
+      tmem_alloc(tmem_holder, 2 * T::kN);
       tmem_relinquish();
     }
   }
@@ -682,11 +727,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       uint32_t phase = 0;
       long issued = 0;
       bool ok = true;
-      const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
+      const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
+      const uint32_t smem0 = smem_u32(smem);
       for (NsSeq s(p); ok && s.next(p);) {
         const int nunits = ns_units(p, s);
         // the first unit and its operands are worked out before the barrier
-        NsUnit n = ns_unit(p, s, first);
+        NsUnit n = ns_unit<T>(p, s, first);
         NsOperand op[2];
         ns_operands(p, s, n.job, op[0], op[1]);
         if (s.ph > 0) {
@@ -696,39 +742,23 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         }
         for (int u = first; ok && u < nunits; u += step) {
           if (u != first) {
-            n = ns_unit(p, s, u);
+            n = ns_unit<T>(p, s, u);
             ns_operands(p, s, n.job, op[0], op[1]);
           }
+          const int rp = n.rt * T::kM, rq = n.ct * T::kN;
+          const int mnp = op[0].template first_mn<T::kM>(rp), mnq = op[1].template first_mn<T::kM>(rq);
+          const NsMaps *mp = op[0].maps, *mq = op[1].maps;
           for (int kb = n.kb0; kb < n.kb1; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
               ok = false;
               break;
             }
-            if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * kNsStageBytes);
-            uint8_t* dst = smem + stage * kNsStageBytes;
-            const uint32_t fb = full0 + stage * 8;
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const int tile = o == 0 ? n.rt : n.ct;
-              const int r0 = tile * kTile + rank * 128;
-              uint8_t* d = dst + o * kNsOpBytes;
-              if (!op[o].is_mn(tile, kb, kTile)) {
-                if (PAIR)
-                  tma_load_3d_pair(d, op[o].k, fb, kb * 64, r0, n.bz);
-                else
-                  tma_load_3d(d, op[o].k, &full[stage], kb * 64, r0, n.bz);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  if (PAIR)
-                    tma_load_3d_pair(d + j * 8192, op[o].mn, fb, r0 + j * 64, kb * 64, n.bz);
-                  else
-                    tma_load_3d(d + j * 8192, op[o].mn, &full[stage], r0 + j * 64, kb * 64, n.bz);
-                }
-              }
-            }
+            if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * T::kStageBytes);
+            const uint32_t dst = smem0 + stage * T::kStageBytes, bar = full0 + stage * 8;
+            ns_load<128, PAIR>(dst, mp, kb >= mnp, rp + rank * 128, kb * 64, n.bz, bar);
+            ns_load<T::kRight, PAIR>(dst + T::kLeftBytes, mq, kb >= mnq, rq + rank * 128, kb * 64, n.bz, bar);
             ++issued;
-            if (++stage == kNsStages) {
+            if (++stage == kStages) {
               stage = 0;
               phase ^= 1u;
             }
@@ -737,10 +767,10 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       }
       // Every copy must have landed before shared memory goes away: the MMA's
       // release of a stage follows its copies.
-      const long n = issued < kNsStages ? issued : kNsStages;
+      const long n = issued < kStages ? issued : kStages;
       for (long i = 0; i < n; ++i) {
         if (stage == 0) {
-          stage = kNsStages - 1;
+          stage = kStages - 1;
           phase ^= 1u;
         } else {
           --stage;
@@ -755,10 +785,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       uint32_t phase = 0;
       int it = 0;
       bool ok = true;
+      const uint32_t smem0 = smem_u32(smem);
+      constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
       for (NsSeq s(p); ok && s.next(p);) {
         const int nunits = ns_units(p, s);
         for (int u = first; ok && u < nunits; u += step, ++it) {
-          const NsUnit n = ns_unit(p, s, u);
+          const NsUnit n = ns_unit<T>(p, s, u);
           NsOperand P, Q;
           ns_operands(p, s, n.job, P, Q);
           const int acc = it & 1;
@@ -767,7 +799,8 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem_base + acc * kTile;
+          const uint32_t d = tmem_base + acc * T::kN;
+          const int mnp = P.template first_mn<T::kM>(n.rt * T::kM), mnq = Q.template first_mn<T::kM>(n.ct * T::kN);
           for (int kb = n.kb0; kb < n.kb1; ++kb) {
             // between two GEMMs this waits as long as the slowest CTA works
             if (!mbar_wait(&full[stage], phase, w)) {
@@ -775,16 +808,19 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
               break;
             }
             tc_fence_after();
-            const bool pm = P.is_mn(n.rt, kb, kTile);
-            const bool qm = Q.is_mn(n.ct, kb, kTile);
-            const uint32_t idesc = idesc_f16_f32(kTile, kTile, pm, qm);
-            const uint32_t a0 = smem_u32(smem + stage * kNsStageBytes);
-            const uint32_t b0 = a0 + kNsOpBytes;
+            const bool pm = kb >= mnp, qm = kb >= mnq;
+            const uint32_t idesc = idesc_f16_f32(T::kM, T::kN, false, false) | (pm ? 1u << 15 : 0u) | (qm ? 1u << 16 : 0u);
+            // The descriptors' low words: address and leading offset (sdesc_sw128)
+            // in units of 16 bytes.  A step is 32 bytes of a K-major row, 16 rows of
+            // 128 bytes of an MN-major block.
+            const uint32_t a0 = (smem0 + stage * T::kStageBytes) >> 4;
+            const uint32_t la = a0 | (pm ? 512u << 16 : 1u << 16);
+            const uint32_t lb = (a0 + (T::kLeftBytes >> 4)) | (qm ? 512u << 16 : 1u << 16);
+            const uint32_t sa = pm ? 128u : 2u, sb = qm ? 128u : 2u;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t ad = pm ? sdesc_sw128(a0 + kk * 2048, 8192, 1024) : sdesc_sw128(a0 + kk * 32, 16, 1024);
-              const uint64_t bd = qm ? sdesc_sw128(b0 + kk * 2048, 8192, 1024) : sdesc_sw128(b0 + kk * 32, 16, 1024);
               const uint32_t accum = (kb != n.kb0 || kk != 0) ? 1u : 0u;
+              const uint64_t ad = f2_bits(la + kk * sa, kDescHigh), bd = f2_bits(lb + kk * sb, kDescHigh);
               // (the kind::f16 instruction; the descriptor says fp16 operands)
               if (PAIR)
                 tc_mma_bf16_pair(d, ad, bd, idesc, accum);
@@ -795,7 +831,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
               tc_commit_pair_mc(&empty[stage], 0x3);
             else
               tc_commit(&empty[stage]);
-            if (++stage == kNsStages) {
+            if (++stage == kStages) {
               stage = 0;
               phase ^= 1u;
             }
@@ -816,7 +852,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     }
   } else {
     NsEpi e;
-    e.stg = sEpi + (warp - 2) * kNsEpiBytes;
+    e.stg = sEpi + (warp - 2) * T::kEpiBytes;
     e.q = warp & 3;  // the TMEM lane quarter this warp may access
     e.half = (warp - 2) >> 2;
     e.rank = rank;
@@ -833,20 +869,20 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       const int nunits = ns_units(p, s);
       const int gen = static_cast<int>(gens >> (16 * s.geo())) & 0xffff;
       gens += 1ull << (16 * s.geo());
-      NsUnit n = ns_unit(p, s, first);
+      NsUnit n = ns_unit<T>(p, s, first);
       // (also without a unit: an arrival must not come before the previous barrier)
       if (s.ph > 0 && !__all_sync(0xffffffffu, mbar_wait(go, (s.ph - 1) & 1, w))) break;
       if (lane == 0) fence_proxy_async_global();
       for (int u = first; ok && u < nunits; u += step, ++it) {
-        if (u != first) n = ns_unit(p, s, u);
+        if (u != first) n = ns_unit<T>(p, s, u);
         const int acc = it & 1;
         const uint32_t par = (it >> 1) & 1;
         if (s.f.kind == kNsSquare)
-          ok = ns_epilogue<kNsSquare, PAIR>(p, s, n, gen, acc, par, tfull, e, w);
+          ok = ns_epilogue<kNsSquare, T>(p, s, n, gen, acc, par, tfull, e, w);
         else if (s.f.kind == kNsUpdate)
-          ok = ns_epilogue<kNsUpdate, PAIR>(p, s, n, gen, acc, par, tfull, e, w);
+          ok = ns_epilogue<kNsUpdate, T>(p, s, n, gen, acc, par, tfull, e, w);
         else
-          ok = ns_epilogue<kNsGram, PAIR>(p, s, n, gen, acc, par, tfull, e, w);
+          ok = ns_epilogue<kNsGram, T>(p, s, n, gen, acc, par, tfull, e, w);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -878,9 +914,9 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   if (warp == 1) {
     tc_fence_after();
     if (PAIR)
-      tmem_dealloc_pair(tmem_base, 2 * kTile);
+      tmem_dealloc_pair(tmem_base, 2 * T::kN);
     else
-      tmem_dealloc(tmem_base, 2 * kTile);
+      tmem_dealloc(tmem_base, 2 * T::kN);
   }
 }
 

@@ -108,7 +108,8 @@ constexpr int kNsMaxCounters = 1 + kGeos * kNsSplitCounters;
 
 struct NsPlan {
   int64_t batch, m, n, s;  // s: the smaller side
-  bool tall, pair;         // pair: 256 x 256 tiles on CTA pairs, else 128 x 128
+  bool tall;
+  int tile;                // 256: 256 x 256 tiles on CTA pairs; 128, 64: 128 x tile
   bool grouped;            // steps in groups of up to three
   int norm_blocks;
   size_t hi[2], lo[2], sym[kBufs], diag[kBufs], sums, counters, part, bytes;
@@ -124,11 +125,16 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
   // CTA pairs where their larger tiles (half of the operand traffic) fill most
   // of the 74 pairs: 224 against 237 us at 1024 x 4096 (64 tiles); with fewer,
   // four times as many small tiles end sooner: 157 against 194 us at 1024 x 1024.
-  p.pair = p.s >= 512 && batch * ((m + 255) / 256) * ((n + 255) / 256) >= 48;
+  // The smallest tiles where they all run at once: 94 against 113 us at 512 x 512, 73 against 91 at
+  // 256 x 256.
+  const int64_t rt = (m + 127) / 128;
+  p.tile = p.s >= 512 && batch * ((m + 255) / 256) * ((n + 255) / 256) >= 48 ? 256
+           : batch * rt * ((n + 63) / 64) <= 148                              ? 64
+                                                                              : 128;
   // Groups save 9 s^2 l operations of five steps and cost 9 s^3 and two more
   // phases: 650 against 1060 us at 2048 x 16384, 322 against 368 at 2048 x 4096
   // (pairs), but 174 against 169 at 1024 x 2048 and 278 against 266 at 2048 x 2048.
-  p.grouped = (p.tall ? m : n) >= (p.pair ? 2 : 3) * p.s;
+  p.grouped = (p.tall ? m : n) >= (p.tile == 256 ? 2 : 3) * p.s;
   const int64_t n8 = m * n / 8;
   p.norm_blocks = static_cast<int>(std::min<int64_t>(kNsMaxNormBlocks, (n8 + 2047) / 2048));
   size_t o = 0;
@@ -149,7 +155,7 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
   p.sums = take(static_cast<size_t>(batch) * p.norm_blocks * 8);
   p.counters = take(kNsMaxCounters * 4);
   // at most one split unit per CTA (pair) of the grid
-  p.part = take(static_cast<size_t>(148) * 128 * (p.pair ? 256 : 128) * 4);
+  p.part = take(p.tile == 64 ? 0 : static_cast<size_t>(148) * 128 * p.tile * 4);
   p.bytes = o;
   return p;
 }
@@ -172,35 +178,41 @@ bool tmap3d(CUtensorMap* m, const void* base, bool bf16, uint64_t cols, uint64_t
   return r == CUDA_SUCCESS;
 }
 
+bool ns_maps(NsMaps* m, const void* base, uint64_t cols, uint64_t rows, uint64_t batch) {
+  return tmap3d(&m->k128, base, false, cols, rows, batch, 128) && tmap3d(&m->b64, base, false, cols, rows, batch, 64);
+}
+
 // A GEMM's tiles over `slots` CTAs (or pairs).  Whole rounds of tiles are one
 // unit each.  A last round that fills at most half of the slots is split by
 // k-blocks, into two parts or, on pairs, four, if they fit and are at least
 // eight k-blocks long: the parts exchange accumulators through memory (about 4
 // us), which costs less than the k-blocks it saves only then.
 NsGeo ns_geo(int64_t batch, int64_t rows, int64_t cols, int64_t K, bool sym, int tile, int slots) {
+  const int tm = tile == 256 ? 256 : 128;
   NsGeo g;
   g.rows = static_cast<int>(rows);
   g.cols = static_cast<int>(cols);
   g.nkb = static_cast<int>((K + 63) / 64);
-  g.n_rt = static_cast<int>((rows + tile - 1) / tile);
+  g.n_rt = static_cast<int>((rows + tm - 1) / tm);
   g.n_ct = static_cast<int>((cols + tile - 1) / tile);
-  g.tiles = sym ? g.n_rt * (g.n_rt + 1) / 2 : g.n_rt * g.n_ct;
+  g.tiles = sym ? g.n_rt * (g.n_rt + 1) / 2 * (tm / tile) : g.n_rt * g.n_ct;
   const int all = static_cast<int>(batch) * g.tiles;
   g.rest = all % slots;
   g.whole = all - g.rest;
   g.splits = 1;
-  while (g.rest > 0 && 2 * g.splits <= (tile == 256 ? 4 : 2) && 2 * g.splits * g.rest <= slots &&
+  while (g.rest > 0 && 2 * g.splits <= tile / 64 && 2 * g.splits * g.rest <= slots &&
          g.nkb / (2 * g.splits) >= 8)
     g.splits *= 2;
   return g;
 }
 
-template <bool PAIR>
+template <int N>
 coda_status_t ns_launch(int dev, DevInfo* info, NsParams& p, const NsPlan& pl, cudaStream_t stream) {
   static bool done[64];
   static int slots[64];  // CTAs (or pairs) resident at once
-  auto kern = ns_kernel<PAIR>;
-  constexpr int kTile = PAIR ? 256 : 128;
+  auto kern = ns_kernel<NsTile<N>>;
+  constexpr bool PAIR = NsTile<N>::kPair;
+  constexpr int kSmem = NsTile<N>::kSmem;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
@@ -210,11 +222,11 @@ coda_status_t ns_launch(int dev, DevInfo* info, NsParams& p, const NsPlan& pl, c
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.blockDim = dim3(kNsThreads, 1, 1);
-  cfg.dynamicSmemBytes = kNsSmemBytes;
+  cfg.dynamicSmemBytes = kSmem;
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (!done[dev]) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmemBytes) != cudaSuccess)
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
         return CODA_ERR_LAUNCH;
       int n = info->sms;
       if (PAIR) {
@@ -228,10 +240,10 @@ coda_status_t ns_launch(int dev, DevInfo* info, NsParams& p, const NsPlan& pl, c
     }
   }
   const int64_t s = pl.s, l = pl.tall ? pl.m : pl.n;
-  p.geo[kGeoGram] = ns_geo(pl.batch, s, s, l, true, kTile, slots[dev]);
-  p.geo[kGeoSym] = ns_geo(pl.batch, s, s, s, true, kTile, slots[dev]);
-  p.geo[kGeoSym2] = ns_geo(2 * pl.batch, s, s, s, true, kTile, slots[dev]);
-  p.geo[kGeoUpdate] = ns_geo(pl.batch, pl.m, pl.n, s, false, kTile, slots[dev]);
+  p.geo[kGeoGram] = ns_geo(pl.batch, s, s, l, true, N, slots[dev]);
+  p.geo[kGeoSym] = ns_geo(pl.batch, s, s, s, true, N, slots[dev]);
+  p.geo[kGeoSym2] = ns_geo(2 * pl.batch, s, s, s, true, N, slots[dev]);
+  p.geo[kGeoUpdate] = ns_geo(pl.batch, pl.m, pl.n, s, false, N, slots[dev]);
   int n = 0;
   for (const NsGeo& g : p.geo) n = std::max(n, g.whole > 0 ? slots[dev] : g.rest * g.splits);
   p.wait_ns = static_cast<uint64_t>(g_wait_ns);
@@ -445,7 +457,7 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
   if (batch == 0) return CODA_OK;
   const NsPlan pl = ns_plan(batch, m, n);
   CODA_CHECK(ws && ws_bytes >= pl.bytes, CODA_ERR_WORKSPACE);
-  CODA_CHECK(2 * batch * ((m + 127) / 128) * ((n + 127) / 128) <= kMaxInt, CODA_ERR_SHAPE);
+  CODA_CHECK(2 * batch * ((m + 127) / 128) * ((n + 63) / 64) <= kMaxInt, CODA_ERR_SHAPE);
   int dev;
   DevInfo* info;
   coda_status_t st = current_device(&dev, &info);
@@ -470,13 +482,12 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
   const int64_t s = pl.s;
   bool ok = true;
   for (int i = 0; i < 2; ++i)
-    ok = ok && tmap3d(&p.Xk[i], hi[i], false, n, m, batch, 128) && tmap3d(&p.Xmn[i], hi[i], false, n, m, batch, 64) &&
-         tmap3d(&p.Hbox[i], hi[i], false, n, m, batch, 32, 32) && tmap3d(&p.Lbox[i], lo[i], false, n, m, batch, 32, 32);
+    ok = ok && ns_maps(&p.X[i], hi[i], n, m, batch) && tmap3d(&p.Hbox[i], hi[i], false, n, m, batch, 32, 32) &&
+         tmap3d(&p.Lbox[i], lo[i], false, n, m, batch, 32, 32);
   for (int i = 0; i < kBufs; ++i) {
     if (!pl.grouped && i != kBufA && i != kBufQ0) continue;
     const void* b = w + pl.sym[i];
-    ok = ok && tmap3d(&p.Sk[i], b, false, s, s, batch, 128) && tmap3d(&p.Smn[i], b, false, s, s, batch, 64) &&
-         tmap3d(&p.Sbox[i], b, false, s, s, batch, 32, 32);
+    ok = ok && ns_maps(&p.S[i], b, s, s, batch) && tmap3d(&p.Sbox[i], b, false, s, s, batch, 32, 32);
   }
   ok = ok && tmap3d(&p.Obox, out, true, n, m, batch, 32, 32);
   if (!ok) return CODA_ERR_INTERNAL;
@@ -489,7 +500,8 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
                   static_cast<double>(eps), hi[0], lo[0], p.counters,
                   kNsMaxCounters);
   if (st != CODA_OK) return st;
-  return pl.pair ? ns_launch<true>(dev, info, p, pl, stm) : ns_launch<false>(dev, info, p, pl, stm);
+  if (pl.tile == 256) return ns_launch<256>(dev, info, p, pl, stm);
+  return pl.tile == 128 ? ns_launch<128>(dev, info, p, pl, stm) : ns_launch<64>(dev, info, p, pl, stm);
 }
 
 }  // extern "C"
