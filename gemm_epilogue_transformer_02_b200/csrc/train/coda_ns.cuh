@@ -62,7 +62,11 @@ constexpr float kNsScaleA = 1024.f;  // A, P A
 constexpr float kNsScaleP = 256.f;   // P, Q
 
 constexpr int kNsEpiWarps = 8;                     // two per TMEM lane quarter, each half of a tile's columns
-constexpr int kNsThreads = 64 + 32 * kNsEpiWarps;  // TMA producer, MMA issuer, epilogue warps
+// Warps: loads of the left operand, MMA issue, epilogue, loads of the right
+// operand.  One thread takes 140 to 220 cycles to issue a copy, and with both
+// operands' 350 and its loop as long as a k-block's MMAs.
+constexpr int kNsThreads = 96 + 32 * kNsEpiWarps;
+constexpr int kNsRightWarp = 2 + kNsEpiWarps;
 constexpr int kNsBoxBytes = 32 * 32 * 2;  // a 32 x 32 box of an epilogue
 
 // A tile's shape and what a CTA keeps for it in shared memory.  N = 256: a
@@ -721,42 +725,50 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   const uint32_t tmem_base = *tmem_holder;
   const WaitCtx w{abort_flag, p.wait_ns};
 
-  if (warp == 0) {
+  if (warp == 0 || warp == kNsRightWarp) {
     if (lane == 0) {
+      const bool left = warp == 0;
       int stage = 0;
       uint32_t phase = 0;
       long issued = 0;
       bool ok = true;
       const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
-      const uint32_t smem0 = smem_u32(smem);
+      const uint32_t smem0 = smem_u32(smem) + (left ? 0 : T::kLeftBytes);
       for (NsSeq s(p); ok && s.next(p);) {
         const int nunits = ns_units(p, s);
-        // the first unit and its operands are worked out before the barrier
+        // the first unit and its operand are worked out before the barrier
         NsUnit n = ns_unit<T>(p, s, first);
-        NsOperand op[2];
-        ns_operands(p, s, n.job, op[0], op[1]);
+        NsOperand P, Q;
+        ns_operands(p, s, n.job, P, Q);
         if (s.ph > 0) {
-          if (!ns_count_wait(p.counters, arrivals * s.ph, w)) break;
+          if (left) {
+            if (!ns_count_wait(p.counters, arrivals * s.ph, w)) break;
+            mbar_arrive(go);
+          } else if (!mbar_wait(go, (s.ph - 1) & 1, w)) {
+            break;
+          }
           fence_proxy_async_global();  // the loads below see what other CTAs' copies wrote
-          mbar_arrive(go);
         }
         for (int u = first; ok && u < nunits; u += step) {
           if (u != first) {
             n = ns_unit<T>(p, s, u);
-            ns_operands(p, s, n.job, op[0], op[1]);
+            ns_operands(p, s, n.job, P, Q);
           }
-          const int rp = n.rt * T::kM, rq = n.ct * T::kN;
-          const int mnp = op[0].template first_mn<T::kM>(rp), mnq = op[1].template first_mn<T::kM>(rq);
-          const NsMaps *mp = op[0].maps, *mq = op[1].maps;
+          const NsOperand op = left ? P : Q;
+          const int row = left ? n.rt * T::kM : n.ct * T::kN;
+          const int mn = op.template first_mn<T::kM>(row), r0 = row + rank * 128;
           for (int kb = n.kb0; kb < n.kb1; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
               ok = false;
               break;
             }
-            if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * T::kStageBytes);
             const uint32_t dst = smem0 + stage * T::kStageBytes, bar = full0 + stage * 8;
-            ns_load<128, PAIR>(dst, mp, kb >= mnp, rp + rank * 128, kb * 64, n.bz, bar);
-            ns_load<T::kRight, PAIR>(dst + T::kLeftBytes, mq, kb >= mnq, rq + rank * 128, kb * 64, n.bz, bar);
+            if (left) {
+              if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * T::kStageBytes);
+              ns_load<128, PAIR>(dst, op.maps, kb >= mn, r0, kb * 64, n.bz, bar);
+            } else {
+              ns_load<T::kRight, PAIR>(dst, op.maps, kb >= mn, r0, kb * 64, n.bz, bar);
+            }
             ++issued;
             if (++stage == kStages) {
               stage = 0;
