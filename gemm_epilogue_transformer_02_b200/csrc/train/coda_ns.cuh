@@ -274,6 +274,17 @@ __device__ __noinline__ bool ns_count_wait(const int* addr, int target, const Wa
   }
 }
 
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Adds to a counter in shared memory and returns its old value; orders this
 // thread's accesses with those of the CTA's other threads that add to it.
 __device__ __forceinline__ int add_acq_rel_cta(int* addr, int v) {
@@ -686,9 +697,9 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* warps_done = reinterpret_cast<int*>(tmem_holder + 2);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // (uniform for the compiler too)
   const int lane = threadIdx.x & 31;
-  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int rank = PAIR ? __shfl_sync(0xffffffffu, static_cast<int>(cluster_ctarank()), 0) : 0;
   const int step = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
   const int first = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
   const int arrivals = static_cast<int>(gridDim.x);  // per phase
@@ -725,74 +736,82 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   const uint32_t tmem_base = *tmem_holder;
   const WaitCtx w{abort_flag, p.wait_ns};
 
+  // The issuing warps run as whole warps, with one elected thread issuing: the
+  // instructions take their operands from uniform registers, and in code of a
+  // single thread every operand is moved there one by one (an MMA loop of 590
+  // cycles a k-block, against 512 of a pair's MMAs).
   if (warp == 0 || warp == kNsRightWarp) {
-    if (lane == 0) {
-      const bool left = warp == 0;
-      int stage = 0;
-      uint32_t phase = 0;
-      long issued = 0;
-      bool ok = true;
-      const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
-      const uint32_t smem0 = smem_u32(smem) + (left ? 0 : T::kLeftBytes);
-      for (NsSeq s(p); ok && s.next(p);) {
-        const int nunits = ns_units(p, s);
-        // the first unit and its operand are worked out before the barrier
-        NsUnit n = ns_unit<T>(p, s, first);
-        NsOperand P, Q;
-        ns_operands(p, s, n.job, P, Q);
-        if (s.ph > 0) {
-          if (left) {
-            if (!ns_count_wait(p.counters, arrivals * s.ph, w)) break;
-            mbar_arrive(go);
-          } else if (!mbar_wait(go, (s.ph - 1) & 1, w)) {
+    const bool left = warp == 0;
+    const bool leader = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;
+    bool ok = true;
+    const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
+    const uint32_t smem0 = smem_u32(smem) + (left ? 0 : T::kLeftBytes);
+    for (NsSeq s(p); ok && s.next(p);) {
+      const int nunits = ns_units(p, s);
+      // the first unit and its operand are worked out before the barrier
+      NsUnit n = ns_unit<T>(p, s, first);
+      NsOperand P, Q;
+      ns_operands(p, s, n.job, P, Q);
+      if (s.ph > 0) {
+        bool passed = true;
+        if (left) {
+          if (leader) passed = ns_count_wait(p.counters, arrivals * s.ph, w);
+          if (leader && passed) mbar_arrive(go);
+        } else {
+          passed = mbar_wait(go, (s.ph - 1) & 1, w);
+        }
+        if (!__all_sync(0xffffffffu, passed)) break;
+        fence_proxy_async_global();  // the loads below see what other CTAs' copies wrote
+      }
+      for (int u = first; ok && u < nunits; u += step) {
+        if (u != first) {
+          n = ns_unit<T>(p, s, u);
+          ns_operands(p, s, n.job, P, Q);
+        }
+        const NsOperand op = left ? P : Q;
+        const int row = left ? n.rt * T::kM : n.ct * T::kN;
+        const int mn = op.template first_mn<T::kM>(row), r0 = row + rank * 128;
+        for (int kb = n.kb0; kb < n.kb1; ++kb) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, w))) {
+            ok = false;
             break;
           }
-          fence_proxy_async_global();  // the loads below see what other CTAs' copies wrote
-        }
-        for (int u = first; ok && u < nunits; u += step) {
-          if (u != first) {
-            n = ns_unit<T>(p, s, u);
-            ns_operands(p, s, n.job, P, Q);
-          }
-          const NsOperand op = left ? P : Q;
-          const int row = left ? n.rt * T::kM : n.ct * T::kN;
-          const int mn = op.template first_mn<T::kM>(row), r0 = row + rank * 128;
-          for (int kb = n.kb0; kb < n.kb1; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
-              ok = false;
-              break;
-            }
-            const uint32_t dst = smem0 + stage * T::kStageBytes, bar = full0 + stage * 8;
+          const uint32_t dst = smem0 + stage * T::kStageBytes, bar = full0 + stage * 8;
+          if (leader) {
             if (left) {
               if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * T::kStageBytes);
               ns_load<128, PAIR>(dst, op.maps, kb >= mn, r0, kb * 64, n.bz, bar);
             } else {
               ns_load<T::kRight, PAIR>(dst, op.maps, kb >= mn, r0, kb * 64, n.bz, bar);
             }
-            ++issued;
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1u;
-            }
+          }
+          if (issued < kStages) ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
       }
-      // Every copy must have landed before shared memory goes away: the MMA's
-      // release of a stage follows its copies.
-      const long n = issued < kStages ? issued : kStages;
-      for (long i = 0; i < n; ++i) {
-        if (stage == 0) {
-          stage = kStages - 1;
-          phase ^= 1u;
-        } else {
-          --stage;
-        }
-        int no_abort = 0;
-        (void)mbar_wait(PAIR ? &empty[stage] : &full[stage], phase, WaitCtx{&no_abort, p.wait_ns});
-      }
     }
+    // Every copy must have landed before shared memory goes away: the MMA's
+    // release of a stage follows its copies.
+    for (int i = 0; i < issued; ++i) {
+      if (stage == 0) {
+        stage = kStages - 1;
+        phase ^= 1u;
+      } else {
+        --stage;
+      }
+      int no_abort = 0;
+      (void)mbar_wait(PAIR ? &empty[stage] : &full[stage], phase, WaitCtx{&no_abort, p.wait_ns});
+    }
+    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool leader = elect_one();
       int stage = 0;
       uint32_t phase = 0;
       int it = 0;
@@ -806,7 +825,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           NsOperand P, Q;
           ns_operands(p, s, n.job, P, Q);
           const int acc = it & 1;
-          if (!mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, w)) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, w))) {
             ok = false;
             break;
           }
@@ -815,7 +834,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           const int mnp = P.template first_mn<T::kM>(n.rt * T::kM), mnq = Q.template first_mn<T::kM>(n.ct * T::kN);
           for (int kb = n.kb0; kb < n.kb1; ++kb) {
             // between two GEMMs this waits as long as the slowest CTA works
-            if (!mbar_wait(&full[stage], phase, w)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, w))) {
               ok = false;
               break;
             }
@@ -829,38 +848,45 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             const uint32_t la = a0 | (pm ? 512u << 16 : 1u << 16);
             const uint32_t lb = (a0 + (T::kLeftBytes >> 4)) | (qm ? 512u << 16 : 1u << 16);
             const uint32_t sa = pm ? 128u : 2u, sb = qm ? 128u : 2u;
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t accum = (kb != n.kb0 || kk != 0) ? 1u : 0u;
-              const uint64_t ad = f2_bits(la + kk * sa, kDescHigh), bd = f2_bits(lb + kk * sb, kDescHigh);
-              // (the kind::f16 instruction; the descriptor says fp16 operands)
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t accum = (kb != n.kb0 || kk != 0) ? 1u : 0u;
+                const uint64_t ad = f2_bits(la + kk * sa, kDescHigh), bd = f2_bits(lb + kk * sb, kDescHigh);
+                // (the kind::f16 instruction; the descriptor says fp16 operands)
+                if (PAIR)
+                  tc_mma_bf16_pair(d, ad, bd, idesc, accum);
+                else
+                  tc_mma_bf16(d, ad, bd, idesc, accum);
+              }
               if (PAIR)
-                tc_mma_bf16_pair(d, ad, bd, idesc, accum);
+                tc_commit_pair_mc(&empty[stage], 0x3);
               else
-                tc_mma_bf16(d, ad, bd, idesc, accum);
+                tc_commit(&empty[stage]);
             }
-            if (PAIR)
-              tc_commit_pair_mc(&empty[stage], 0x3);
-            else
-              tc_commit(&empty[stage]);
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1u;
             }
           }
           if (!ok) break;
-          if (PAIR)
-            tc_commit_pair_mc(&tfull[acc], 0x3);
-          else
-            tc_commit(&tfull[acc]);
+          if (leader) {
+            if (PAIR)
+              tc_commit_pair_mc(&tfull[acc], 0x3);
+            else
+              tc_commit(&tfull[acc]);
+          }
         }
       }
-      if (PAIR)
-        tc_commit_pair(drain);
-      else
-        tc_commit(drain);
+      if (leader) {
+        if (PAIR)
+          tc_commit_pair(drain);
+        else
+          tc_commit(drain);
+      }
       int no_abort = 0;
       (void)mbar_wait(drain, 0, WaitCtx{&no_abort, p.wait_ns});
+      __syncwarp();
     }
   } else {
     NsEpi e;
