@@ -27,7 +27,7 @@
 // 3 s^2 l + s^3 operations, five of them as groups of 3 and 2 cost 6 s^2 l +
 // 14 s^3 instead of 15 s^2 l + 5 s^3.  Rounding A' instead of forming X' X'^T
 // loses the smallest singular values sooner, so a group is at most three steps,
-// later ones two, and they are only used where l is 2 or 3 times s or more.
+// later ones two, and they are only used from l >= 2 s on.
 //
 // Precision.  Operands are fp16, not bf16: with |X|_F = 1 every value is
 // bounded, so scaled by powers of two they use fp16's 11 bits where bf16 would

@@ -122,19 +122,23 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
   p.n = n;
   p.tall = m > n;
   p.s = p.tall ? n : m;
-  // CTA pairs where their larger tiles (half of the operand traffic) fill most
-  // of the 74 pairs: 224 against 237 us at 1024 x 4096 (64 tiles); with fewer,
-  // four times as many small tiles end sooner: 157 against 194 us at 1024 x 1024.
-  // The smallest tiles where they all run at once: 94 against 113 us at 512 x 512, 73 against 91 at
-  // 256 x 256.
-  const int64_t rt = (m + 127) / 128;
-  p.tile = p.s >= 512 && batch * ((m + 255) / 256) * ((n + 255) / 256) >= 48 ? 256
-           : batch * rt * ((n + 63) / 64) <= 148                              ? 64
-                                                                              : 128;
+  // CTA pairs (half of the operand traffic) where K is long and their 256 x 256
+  // tiles fill more than one round of the 74 pairs: 333 against 434 us for two of
+  // 2048 x 2048, 1040 against 1420 at 4096 x 4096.  With fewer tiles or a short K
+  // the four times as many small ones end sooner: 171 against 213 us at 1024 x
+  // 4096, 269 against 311 for eight of 1024 x 1024, 245 against 249 at 2048 x
+  // 2048; 512 tiles of K 1024 425 against 458 us, 256 of them 311 against 290.
+  // The smallest where all of them run at once: 94 against 113 us at 512 x
+  // 512, 73 against 91 at 256 x 256.
+  const int64_t t256 = batch * ((m + 255) / 256) * ((n + 255) / 256);
+  p.tile = t256 >= (p.s >= 1536 ? 100 : 400) && p.s >= 1024        ? 256
+           : batch * ((m + 127) / 128) * ((n + 63) / 64) <= 148 ? 64
+                                                                : 128;
   // Groups save 9 s^2 l operations of five steps and cost 9 s^3 and two more
-  // phases: 650 against 1060 us at 2048 x 16384, 322 against 368 at 2048 x 4096
-  // (pairs), but 174 against 169 at 1024 x 2048 and 278 against 266 at 2048 x 2048.
-  p.grouped = (p.tall ? m : n) >= (p.tile == 256 ? 2 : 3) * p.s;
+  // phases: 650 against 1060 us at 2048 x 16384, 298 against 367 at 2048 x 4096,
+  // 164 against 173 at 1024 x 2560, but 152 against 148 at 1024 x 2048 and 267
+  // against 249 at 2048 x 2048.
+  p.grouped = (p.tall ? m : n) >= 2 * p.s;
   const int64_t n8 = m * n / 8;
   p.norm_blocks = static_cast<int>(std::min<int64_t>(kNsMaxNormBlocks, (n8 + 2047) / 2048));
   size_t o = 0;
