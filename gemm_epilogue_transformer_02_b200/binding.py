@@ -877,7 +877,7 @@ def embed(tokens, E, scale: float = 1.0, gamma=None, *, h=True, partial=True, h_
     elif hg_out is not None:
         raise ValueError("hg_out needs gamma")
     h_out = _out(h_out, BF16, "h_out", (M, D), E) if h else None
-    partial_out = _out(partial_out, F32, "partial_out", (-(-D // 128), M), E) if partial else None
+    partial_out = _out(partial_out, F32, "partial_out", (partial_cols(D), M), E) if partial else None
     _launch("coda_embed", (E, tokens, gamma, h_out, hg_out, partial_out), tokens.data_ptr(), E.data_ptr(), scale,
             _addr(gamma), _addr(h_out), _addr(hg_out), _addr(partial_out), M, D, V)
     return h_out, hg_out, partial_out

@@ -27,7 +27,7 @@
 // 3 s^2 l + s^3 operations, five of them as groups of 3 and 2 cost 6 s^2 l +
 // 14 s^3 instead of 15 s^2 l + 5 s^3.  Rounding A' instead of forming X' X'^T
 // loses the smallest singular values sooner, so a group is at most three steps,
-// later ones two, and they are only used from l >= 2 s on.
+// later ones two, and they are only used from s = 512 and l = 2 s on.
 //
 // Precision.  Operands are fp16, not bf16: with |X|_F = 1 every value is
 // bounded, so scaled by powers of two they use fp16's 11 bits where bf16 would
@@ -43,9 +43,11 @@
 //     the GEMMs read the high part, and the diagonal of P (all of P where X is
 //     small) multiplies the low part too.  The last update drops it.
 // Against 64 bits this gives 0.3e-3 to 1.1e-3 of |X|_F for Gaussian and
-// correlated matrices after five steps, and up to 3e-3 (in groups 7e-3) for
-// nearly low-rank ones; plain bf16 products give 0.9e-2 and 3e-1.  The bf16
-// rounding of the output alone is 1.7e-3.
+// correlated matrices after five steps.  Nearly low-rank ones (a few directions
+// hold the norm, the others grow by 3.4^5 from a hundredth of them) come to 1e-3
+// to 3e-3, in groups to 1e-2: there A's rounding, relative to its large entries,
+// grows with the small directions.  Plain bf16 products give 0.9e-2 and 3e-1.
+// The bf16 rounding of the output alone is 1.7e-3.
 #pragma once
 
 #include <cuda_fp16.h>

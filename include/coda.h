@@ -563,7 +563,9 @@ size_t coda_newton_schulz_workspace_size(int64_t batch, int64_t m, int64_t n);
  * and out = bf16(X).  G [batch, m, n] fp32 (a gradient or momentum, such as the
  * backward calls give), out [batch, m, n] bf16.  The products take fp16
  * operands with fp32 sums and corrections for their rounding: about 1e-3 of
- * |X|_F from exact arithmetic before the output's rounding.  The coefficients
+ * |X|_F from exact arithmetic before the output's rounding; up to 1e-2 for a
+ * nearly low-rank G whose larger side is at least twice the smaller one (of 512
+ * or more), where several steps are taken on the smaller side.  The coefficients
  * must keep the singular values bounded, as Muon's (3.4445, -4.775, 2.0315)
  * do: intermediate values beyond 16 (X) or 64 (A, b A + c A^2) become
  * infinite.  A matrix with a non-finite entry gives a non-finite result and

@@ -169,6 +169,22 @@ def test_embed_bwd_empty_batch():
     assert not bool(dE.any())
 
 
+def test_empty_batches():
+    """No rows (their tensors have no address): nothing is launched or refused."""
+    e = torch.empty(0, 256, dtype=BF, device="cuda")
+    g = torch.ones(256, dtype=BF, device="cuda")
+    h, hg, partial = C.embed(torch.empty(0, dtype=torch.int64, device="cuda"), g.view(1, 256), 1.0, g)
+    assert h.shape == hg.shape == (0, 256) and partial.shape == (2, 0)
+    h, q, sf, r = C.add_rmsnorm_mx(e, e, g, 1e-6)
+    assert h.shape == q.shape == (0, 256) and sf.numel() == r.numel() == 0
+    amax = torch.full((1,), 3.0, device="cuda")
+    _, q8, _, _ = C.add_rmsnorm_fp8(e, None, g, 1e-6, torch.ones(1, device="cuda"), amax_out=amax)
+    assert q8.shape == (0, 256) and float(amax) == 3.0
+    dx, dgamma = C.add_rmsnorm_bwd(e, e, torch.empty(0, device="cuda"), g, e)
+    assert dx.shape == (0, 256) and not bool(dgamma.any())
+    assert C.newton_schulz(torch.empty(0, 64, 128, device="cuda")).shape == (0, 64, 128)
+
+
 # --------------------------------------------------------------- 8-bit norm
 
 
@@ -345,15 +361,16 @@ def ns_tol(steps):
     return U_BF + 2 * math.sqrt(3 * steps) * U_16
 
 
-def ns_check(out, G, steps=5, **kw):
+def ns_check(out, G, steps=5, more=0.0, **kw):
     ref = ns_ref(G, steps, **kw)
     err = (out.to(F64) - ref).flatten(-2).norm(dim=-1) / ref.flatten(-2).norm(dim=-1).clamp(min=1e-300)
-    assert bool((err <= ns_tol(steps)).all()), err
+    assert bool((err <= ns_tol(steps) + more).all()), err
     return err
 
 
 @pytest.mark.parametrize("m,n", [(8, 8), (8, 1000), (72, 8), (128, 128), (136, 264), (264, 136), (512, 512),
-                                 (1000, 264), (136, 1032), (1024, 1024), (1096, 1032), (1032, 2056), (2056, 1032)])
+                                 (1000, 264), (136, 1032), (1024, 1024), (1096, 1032), (1032, 2056), (2056, 1032),
+                                 (1544, 4104), (4104, 1544), (2056, 2568)])
 @pytest.mark.parametrize("batch", [None, 3])
 def test_newton_schulz(m, n, batch):
     g = gen(m + n)
@@ -382,6 +399,33 @@ def test_newton_schulz_nearly_low_rank(m, n):
     G = randn(g, m, 16) @ randn(g, 16, n) + 0.01 * randn(g, m, n)
     ns_check(C.newton_schulz(G), G)
     ns_check(C.newton_schulz(G.t().contiguous()), G.t())
+
+
+@pytest.mark.parametrize("m,n", [(512, 2048), (1024, 2560)])
+def test_newton_schulz_nearly_low_rank_in_groups(m, n):
+    """Steps 1-3 and 4-5 are taken on the Gram matrix A.  Its fp16 rounding is a
+    symmetric matrix of spectral norm e <= 2 |A|_F 2^-12 / sqrt(m) (entries off by
+    2^-12 of theirs in random directions), which the small directions take
+    through the later steps of a group, growing by a^2 = 11.9 a step, and which
+    moves P by |b| e / a = 1.4 e of itself.  16 directions hold the norm: |A|_F is
+    1/4 at first and at most 4 * 1.44 in the second group, so for m >= 512 that
+    is 1.4 * 5.4e-6 * 11.9^2 + 1.4 * 1.25e-4 * 11.9 = 3.2e-3; P A and A' are
+    rounded in the same way: sqrt(3) of that, and sqrt(2) for the mirrored half."""
+    g = gen(18)
+    G = randn(g, m, 16) @ randn(g, 16, n) + 0.01 * randn(g, m, n)
+    more = math.sqrt(6) * 3.2e-3
+    ns_check(C.newton_schulz(G), G, more=more)
+    ns_check(C.newton_schulz(G.t().contiguous()), G.t(), more=more)
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 9])
+def test_newton_schulz_groups_of_every_length(steps):
+    """Wide enough for groups: 1, 2, 3, 3 + 1, 3 + 2 + 1, 3 + 2 + 2 + 2 steps; odd
+    sizes, and a batch."""
+    G = randn(gen(40 + steps), 2, 520, 1048)
+    ns_check(C.newton_schulz(G, steps=steps), G, steps)
+    T = G.mT.contiguous()
+    ns_check(C.newton_schulz(T, steps=steps), T, steps)
 
 
 def test_newton_schulz_scale():
