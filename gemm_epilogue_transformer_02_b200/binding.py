@@ -818,6 +818,9 @@ def block_backward(dOut, x, W1, W2, gamma, fwd):
 # combined test per tensor, and the errors' wording only where it fails.
 
 
+PARTIAL_TILE = 128  # partial_tile_width(): columns of a slot of the partial sums
+
+
 def _ok(t, dtype, name, shape):
     """_need with a shape, in one test where all is well."""
     if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_cuda
@@ -827,15 +830,23 @@ def _ok(t, dtype, name, shape):
 
 
 def _matrix(t, dtype, name):
-    _need(t, dtype, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape if isinstance(t, torch.Tensor) else None
+    _ok(t, dtype, name, shape)
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got shape {tuple(shape)}")
+    return shape
 
 
 def _out(t, dtype, name, shape, like):
-    """An output: the caller's, or a new one."""
+    """An output: the caller's, or a new one on the device of `like`."""
     return like.new_empty(shape, dtype=dtype) if t is None else _ok(t, dtype, name, shape)
+
+
+def _out_like(t, name, like, dtype=None):
+    """The same of the shape (and, without one given, the type) of `like`, which is quicker to make."""
+    if t is None:
+        return torch.empty_like(like) if dtype is None else torch.empty_like(like, dtype=dtype)
+    return _ok(t, dtype or like.dtype, name, like.shape)
 
 
 def _workspace(ws, nbytes: int, like):
@@ -850,7 +861,7 @@ def _launch(name: str, tensors, *args):
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: tensors on different devices: "
                              + ", ".join(str(t.device) for t in tensors if t is not None))
-    if dev == torch._C._cuda_getDevice():
+    if dev == torch._C._cuda_getDevice():  # (the public forms of these two calls take 4 us together)
         _call(name, *args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -868,16 +879,15 @@ def embed(tokens, E, scale: float = 1.0, gamma=None, *, h=True, partial=True, h_
     after rms_reduce, of gemm_swiglu.  tokens [M] int64; one outside [0, V)
     gives a zero row.  Returns (h, hg, partial); entries not requested are None."""
     V, D = _matrix(E, BF16, "E")
-    _need(tokens, torch.int64, "tokens")
-    M = tokens.numel()
+    M = tokens.numel() if isinstance(tokens, torch.Tensor) else 0
     _ok(tokens, torch.int64, "tokens", (M,))
+    h_out = _out(h_out, BF16, "h_out", (M, D), E) if h else None
     if gamma is not None:
         _ok(gamma, BF16, "gamma", (D,))
-        hg_out = _out(hg_out, BF16, "hg_out", (M, D), E)
+        hg_out = _out(hg_out, BF16, "hg_out", (M, D), E) if h_out is None else _out_like(hg_out, "hg_out", h_out)
     elif hg_out is not None:
         raise ValueError("hg_out needs gamma")
-    h_out = _out(h_out, BF16, "h_out", (M, D), E) if h else None
-    partial_out = _out(partial_out, F32, "partial_out", (partial_cols(D), M), E) if partial else None
+    partial_out = _out(partial_out, F32, "partial_out", (-(-D // PARTIAL_TILE), M), E) if partial else None
     _launch("coda_embed", (E, tokens, gamma, h_out, hg_out, partial_out), tokens.data_ptr(), E.data_ptr(), scale,
             _addr(gamma), _addr(h_out), _addr(hg_out), _addr(partial_out), M, D, V)
     return h_out, hg_out, partial_out
@@ -906,9 +916,10 @@ def add_rmsnorm_mx(x, res, gamma, eps: float, *, h=True, h_out=None, yq_out=None
     if res is not None:
         _ok(res, BF16, "res", (M, N))
     _ok(gamma, BF16, "gamma", (N,))
-    h_out = _out(h_out, BF16, "h_out", (M, N), x) if h else None
-    yq_out = _out(yq_out, U8, "yq_out", (M, N), x)
-    ysf_out = _out(ysf_out, U8, "ysf_out", (mx_sf_bytes(M, N, MX_A) if M else 0,), x)
+    h_out = _out_like(h_out, "h_out", x) if h else None
+    yq_out = _out_like(yq_out, "yq_out", x, U8)
+    nsf = N // 128 * (-(-M // 128)) * 512 if N % 128 == 0 else mx_sf_bytes(M, N, MX_A)  # (which raises)
+    ysf_out = _out(ysf_out, U8, "ysf_out", (nsf,), x)
     r_out = _out(r_out, F32, "r_out", (M,), x)
     _launch("coda_add_rmsnorm_mx", (x, res, gamma, h_out, yq_out, ysf_out, r_out), x.data_ptr(), _addr(res),
             gamma.data_ptr(), eps, _addr(h_out), yq_out.data_ptr(), ysf_out.data_ptr(), r_out.data_ptr(), M, N)
@@ -924,9 +935,9 @@ def add_rmsnorm_fp8(x, res, gamma, eps: float, s_y, *, h=True, h_out=None, y8_ou
         _ok(res, BF16, "res", (M, N))
     _ok(gamma, BF16, "gamma", (N,))
     _ok(s_y, F32, "s_y", (1,))
-    h_out = _out(h_out, BF16, "h_out", (M, N), x) if h else None
-    y8_out = _out(y8_out, U8, "y8_out", (M, N), x)
-    amax_out = _out(amax_out, F32, "amax_out", (1,), x)
+    h_out = _out_like(h_out, "h_out", x) if h else None
+    y8_out = _out_like(y8_out, "y8_out", x, U8)
+    amax_out = _out_like(amax_out, "amax_out", s_y)
     r_out = _out(r_out, F32, "r_out", (M,), x)
     _launch("coda_add_rmsnorm_fp8", (x, res, gamma, s_y, h_out, y8_out, amax_out, r_out), x.data_ptr(), _addr(res),
             gamma.data_ptr(), eps, s_y.data_ptr(), _addr(h_out), y8_out.data_ptr(), amax_out.data_ptr(),
@@ -944,8 +955,8 @@ def add_rmsnorm_bwd(dy, h, r, gamma, d_h=None, dx_out=None, dgamma_out=None, ws=
     _ok(gamma, BF16, "gamma", (N,))
     if d_h is not None:
         _ok(d_h, BF16, "d_h", (M, N))
-    dx_out = _out(dx_out, BF16, "dx_out", (M, N), dy)
-    dgamma_out = _out(dgamma_out, F32, "dgamma_out", (N,), dy)
+    dx_out = _out_like(dx_out, "dx_out", dy)
+    dgamma_out = _out_like(dgamma_out, "dgamma_out", gamma, F32)
     ws = _workspace(ws, load_library().coda_add_rmsnorm_bwd_workspace_size(M, N), dy)
     _launch("coda_add_rmsnorm_bwd", (dy, h, r, gamma, d_h, dx_out, dgamma_out, ws), dy.data_ptr(), h.data_ptr(),
             r.data_ptr(), gamma.data_ptr(), _addr(d_h), dx_out.data_ptr(), dgamma_out.data_ptr(), ws.data_ptr(),
@@ -966,7 +977,7 @@ def newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: float = 1
     a, b, c = coeffs
     batch = G.shape[0] if G.dim() == 3 else 1
     m, n = G.shape[-2:]
-    out = _out(out, BF16, "out", G.shape, G)
+    out = _out_like(out, "out", G, BF16)
     ws = _workspace(ws, load_library().coda_newton_schulz_workspace_size(batch, m, n), G)
     _launch("coda_newton_schulz", (G, out, ws), G.data_ptr(), out.data_ptr(), batch, m, n, steps, a, b, c, eps,
             ws.data_ptr(), ws.numel())

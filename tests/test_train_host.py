@@ -130,6 +130,11 @@ def test_newton_schulz_refusals(lib):
         assert f(P, Q, b, m, k, steps, *c, eps, R, BIG, None) == SHAPE
 
 
+def test_binding_constants(lib):
+    assert C.PARTIAL_TILE == C.partial_tile_width()
+    assert lib.coda_version() >= 4
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes(lib):
     x = torch.zeros(4, 128, dtype=torch.bfloat16)
     t = torch.zeros(4, dtype=torch.int64)
