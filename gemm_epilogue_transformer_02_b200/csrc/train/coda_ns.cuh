@@ -69,6 +69,9 @@ constexpr int kNsEpiWarps = 8;                     // two per TMEM lane quarter,
 // operands' 350 and its loop as long as a k-block's MMAs.
 constexpr int kNsThreads = 96 + 32 * kNsEpiWarps;
 constexpr int kNsRightWarp = 2 + kNsEpiWarps;
+// The loads of a unit are at most this many units ahead of its epilogue (eight
+// stages of one k-block each, and two accumulators).
+constexpr int kNsAhead = 16;
 constexpr int kNsBoxBytes = 32 * 32 * 2;  // a 32 x 32 box of an epilogue
 
 // A tile's shape and what a CTA keeps for it in shared memory.  N = 256: a
@@ -91,8 +94,8 @@ struct NsTile {
   static constexpr int kBufs = kBlks > 1 ? 2 : 1;                      // its staging buffers: a high and a low box
   static constexpr int kEpiBytes = kBufs * 2 * kNsBoxBytes;
   static constexpr int kWarps = (kPair ? 2 : 1) * kNsEpiWarps;         // epilogue warps of a tile
-  static constexpr int kBars = 2 * kStages + 2 + 2 + 1 + 1 + 2 * kNsEpiWarps;
-  static constexpr int kSmem = 1024 + kStages * kStageBytes + kNsEpiWarps * kEpiBytes + kBars * 8 + 32;
+  static constexpr int kBars = 2 * kStages + 2 + 2 + 1 + kNsAhead + 2 * kNsEpiWarps;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kNsEpiWarps * kEpiBytes + kBars * 8 + kNsAhead * 4 + 32;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -106,6 +109,7 @@ struct NsGeo {
   int whole;              // the first `whole` tiles are one unit each,
   int rest;               // the other `rest` tiles
   int splits;             // are `splits` units each, over equal shares of the k-blocks
+  int arrivals;           // at each matrix's counter in one such phase
 };
 enum NsGeoIndex : int { kGeoGram = 0, kGeoSym, kGeoSym2, kGeoUpdate, kGeos };
 
@@ -128,16 +132,18 @@ struct NsParams {
   CUtensorMap Hbox[2], Lbox[2], Sbox[kBufs], Obox;
   float2* diag[kBufs];  // [batch, s]: (d, f): what fp16 drops of the diagonal, and the rounded diagonal
   float* part;          // partial accumulators of the split tiles
-  int* counters;        // [0]: arrivals at the grid barrier; then for each geometry arrivals at the split tiles' parts
+  int* counters;        // [batch]: arrivals of finished units: of each matrix (if few), or of all at the first;
+                        // then for each geometry those of the split tiles' parts
   NsGeo geo[kGeos];
   int batch, steps, tall;
+  int few;              // a unit waits for its own matrix (else for all of them)
   int first, later;     // steps of the first group and of later ones, at most
   float a, b, c;
   uint64_t wait_ns;
 };
 
-// The phases of a group of one, two or three steps, with a grid barrier after
-// each.  A phase is a GEMM (or two products side by side: `two`) given by its
+// The phases of a group of one, two or three steps.  A matrix's phase begins when
+// its last one is complete.  A phase is a GEMM (or two products side by side: `two`) given by its
 // symmetric matrices: left, right, result.
 struct NsPhase {
   uint8_t kind, two;
@@ -165,10 +171,11 @@ struct NsSeq {
   int group = 0;   // X of this group is in buffer group & 1
   int left, size;  // steps left, this group's included; its steps
   int pos = -1;
+  unsigned done = 0;  // arrivals of a matrix's units in the phases before this one
   NsPhase f;
   __device__ __forceinline__ explicit NsSeq(const NsParams& p) : left(p.steps), size(min(p.first, p.steps)) {}
   __device__ __forceinline__ bool next(const NsParams& p) {
-    ++ph;
+    if (++ph > 0) done += static_cast<unsigned>(p.geo[geo()].arrivals);
     if (++pos == kNsPhaseCount[size - 1]) {
       left -= size;
       if (left == 0) return false;
@@ -180,7 +187,6 @@ struct NsSeq {
     return true;
   }
   __device__ __forceinline__ bool last_group() const { return left == size; }
-  __device__ __forceinline__ bool last_phase() const { return left == size && f.kind == kNsUpdate; }
   __device__ __forceinline__ int geo() const {
     return f.kind == kNsGram ? kGeoGram : (f.kind == kNsUpdate ? kGeoUpdate : (f.two ? kGeoSym2 : kGeoSym));
   }
@@ -259,12 +265,12 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
 }
 __device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) { return f2_fma(b, f2_set(-1.f, -1.f), a); }
 
-// Wait (bounded) until *addr >= target, polling without a pause: few threads
+// Wait (bounded) until *addr has reached target (both count modulo 2^32), polling without a pause: few threads
 // wait, and each poll takes a trip to L2.
-__device__ __noinline__ bool ns_count_wait(const int* addr, int target, const WaitCtx& w) {
+__device__ __noinline__ bool ns_count_wait(const int* addr, unsigned target, const WaitCtx& w) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (ld_acquire(addr) >= target) return true;
+    if (static_cast<int>(static_cast<unsigned>(ld_acquire(addr)) - target) >= 0) return true;
     if ((i & 63u) == 0) {
       if (*w.abort_flag) return false;
       if (globaltimer_ns() - t0 > w.limit_ns) {
@@ -301,6 +307,7 @@ struct NsUnit {
   int kb0, kb1;
   int part;   // which of a split tile's parts (-1: a whole tile)
   int split;  // the split tile's number
+  int weight;  // of its arrival: those of one tile make `splits`
 };
 
 // A symmetric result takes the square blocks on and below the diagonal, row by
@@ -312,6 +319,7 @@ __device__ __forceinline__ NsUnit ns_unit_of(const NsGeo& g, int batch, int u) {
   int t = u;
   n.part = -1;
   n.split = 0;
+  n.weight = g.splits;
   n.kb0 = 0;
   n.kb1 = g.nkb;
   if (u >= g.whole) {
@@ -320,6 +328,7 @@ __device__ __forceinline__ NsUnit ns_unit_of(const NsGeo& g, int batch, int u) {
     t = g.whole + n.split;
     if (g.splits > 1) {
       n.part = k;
+      n.weight = 1;
       n.kb0 = g.nkb * k / g.splits;
       n.kb1 = g.nkb * (k + 1) / g.splits;
     }
@@ -356,6 +365,15 @@ __device__ __forceinline__ NsUnit ns_unit(const NsParams& p, const NsSeq& s, int
 __device__ __forceinline__ int ns_units(const NsParams& p, const NsSeq& s) {
   const NsGeo& g = p.geo[s.geo()];
   return g.whole + g.rest * g.splits;
+}
+
+// What unit n has to wait for that the CTA's last one of the phase (waited: -1 for
+// the first) did not: a matrix, all of them (p.batch), or nothing (-1).
+__device__ __forceinline__ int ns_need(const NsParams& p, const NsSeq& s, const NsUnit& n, int& waited) {
+  const int need = p.few && n.part < 0 ? n.bz : p.batch;
+  if (s.ph == 0 || need == waited || waited == p.batch) return -1;
+  waited = need;
+  return need;
 }
 
 // An operand of one GEMM.  Of a symmetric matrix the blocks of M x M on and below
@@ -521,7 +539,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
     __syncwarp();
     int ok = 1;
     if (lane == 0) {
-      int* c = p.counters + 1 + gi * kNsSplitCounters + n.split * T::kWarps + region;
+      int* c = p.counters + p.batch + gi * kNsSplitCounters + n.split * T::kWarps + region;
       red_release_add(c, 1);
       if (b0 < b1) ok = ns_count_wait(c, g.splits * (gen + 1), w) ? 1 : 0;
     }
@@ -676,11 +694,22 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
 }
 
 // All steps in one persistent launch.  The CTAs (or CTA pairs) take the units of
-// a GEMM in turn; between two GEMMs all of them wait for each other at a counter
-// in global memory: a CTA arrives when the stores of its last epilogue warp have
-// completed; its producer thread polls the counter, loads on, and lets the
-// epilogue warps go on through an mbarrier.  All CTAs have to be resident at
-// once, so the launch is a cooperative one.
+// a phase in turn, and go from phase to phase.  A unit loads what other CTAs
+// wrote in the phase before: a CTA arrives at a counter in global memory when
+// its epilogue warps' stores have completed, and the thread that issues a unit's
+// left loads polls until the last phase is complete, and lets the other loads and
+// the epilogue warps go on through an mbarrier.  One counter for all matrices
+// makes that a barrier between GEMMs, and the CTAs arrive once for a phase.  With
+// a few units for each CTA (`few`) each matrix has its own, and the last units of
+// one phase run beside the first of the next: 575 against 626 us for four of 2048
+// x 2048, 239 against 264 for eight of 1024 x 1024, 128 against 154 for sixteen of
+// 512 x 512 (but 90.8 against 88.9 for four of them, one unit for each CTA).  With
+// many units the phases' ends matter less than an arrival for each unit: 64 of
+// 512 x 512 took 415 against 390.  Every buffer is written one phase or more
+// after the phases that read it, of the same matrix.  The split tiles' exchange
+// buffers are no matrix's: their units wait for all matrices.  A unit only waits
+// for units before it in the order that all CTAs follow, and all CTAs are
+// resident at once, by a cooperative launch.
 template <class T>
 __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant__ NsParams p) {
   constexpr bool PAIR = T::kPair;
@@ -693,18 +722,17 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint64_t* go = drain + 1;  // the grid barrier after each GEMM, for this CTA's epilogue warps
-  uint64_t* ebars = go + 1;  // two for each epilogue warp
+  uint64_t* go = drain + 1;         // the i-th wait of this CTA is over: barrier i mod kNsAhead
+  uint64_t* ebars = go + kNsAhead;  // two for each epilogue warp
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(ebars + 2 * kNsEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* warps_done = reinterpret_cast<int*>(tmem_holder + 2);
+  int* warps_done = reinterpret_cast<int*>(tmem_holder + 2);  // [kNsAhead]: epilogue warps done with unit i
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // (uniform for the compiler too)
   const int lane = threadIdx.x & 31;
   const int rank = PAIR ? __shfl_sync(0xffffffffu, static_cast<int>(cluster_ctarank()), 0) : 0;
   const int step = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
   const int first = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
-  const int arrivals = static_cast<int>(gridDim.x);  // per phase
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -716,10 +744,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       mbar_init(&tempty[a], PAIR ? 2 * kNsEpiWarps : kNsEpiWarps);
     }
     mbar_init(drain, 1);
-    mbar_init(go, 1);
+    for (int i = 0; i < kNsAhead; ++i) {
+      mbar_init(&go[i], 1);
+      warps_done[i] = 0;
+    }
     for (int i = 0; i < 2 * kNsEpiWarps; ++i) mbar_init(&ebars[i], 1);
     *abort_flag = 0;
-    *warps_done = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -748,34 +778,41 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     int stage = 0;
     uint32_t phase = 0;
     int issued = 0;
+    int it = 0;  // waits so far
     bool ok = true;
     const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
     const uint32_t smem0 = smem_u32(smem) + (left ? 0 : T::kLeftBytes);
     for (NsSeq s(p); ok && s.next(p);) {
       const int nunits = ns_units(p, s);
-      // the first unit and its operand are worked out before the barrier
-      NsUnit n = ns_unit<T>(p, s, first);
-      NsOperand P, Q;
-      ns_operands(p, s, n.job, P, Q);
-      if (s.ph > 0) {
-        bool passed = true;
-        if (left) {
-          if (leader) passed = ns_count_wait(p.counters, arrivals * s.ph, w);
-          if (leader && passed) mbar_arrive(go);
-        } else {
-          passed = mbar_wait(go, (s.ph - 1) & 1, w);
-        }
-        if (!__all_sync(0xffffffffu, passed)) break;
-        fence_proxy_async_global();  // the loads below see what other CTAs' copies wrote
-      }
+      int waited = -1;
       for (int u = first; ok && u < nunits; u += step) {
-        if (u != first) {
-          n = ns_unit<T>(p, s, u);
-          ns_operands(p, s, n.job, P, Q);
-        }
-        const NsOperand op = left ? P : Q;
+        const NsUnit n = ns_unit<T>(p, s, u);
+        NsOperand P, Q;
+        ns_operands(p, s, n.job, P, Q);
+        NsOperand op = left ? P : Q;
         const int row = left ? n.rt * T::kM : n.ct * T::kN;
-        const int mn = op.template first_mn<T::kM>(row), r0 = row + rank * 128;
+        int mn = op.template first_mn<T::kM>(row), r0 = row + rank * 128;
+        asm volatile("" : "+l"(op.maps), "+r"(mn), "+r"(r0));  // worked out before the wait, not after it
+        const int need = ns_need(p, s, n, waited);
+        if (need >= 0) {
+          bool passed = true;
+          if (left) {
+            const int b0 = need < p.batch ? need : 0, b1 = need < p.batch ? need + 1 : (p.few ? p.batch : 1);
+            const unsigned target = p.few ? s.done : s.done * static_cast<unsigned>(p.batch);
+            for (int b = b0 + lane; b < b1; b += 32) passed = passed && ns_count_wait(p.counters + b, target, w);
+            if (b1 - b0 > 1) passed = __all_sync(0xffffffffu, passed);
+            if (lane == 0 && passed) mbar_arrive(&go[it & (kNsAhead - 1)]);
+          } else {
+            passed = mbar_wait(&go[it & (kNsAhead - 1)], (it / kNsAhead) & 1, w);
+          }
+          if (!__all_sync(0xffffffffu, passed)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          fence_proxy_async_global();  // the loads below see what other CTAs' copies wrote
+          ++it;
+        }
         for (int kb = n.kb0; kb < n.kb1; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, w))) {
             ok = false;
@@ -904,17 +941,23 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
     int it = 0;
     bool ok = true;
+    int waits = 0;
     uint64_t gens = 0;  // phases of each geometry so far, 16 bits each
     for (NsSeq s(p); ok && s.next(p);) {
       const int nunits = ns_units(p, s);
       const int gen = static_cast<int>(gens >> (16 * s.geo())) & 0xffff;
       gens += 1ull << (16 * s.geo());
-      NsUnit n = ns_unit<T>(p, s, first);
-      // (also without a unit: an arrival must not come before the previous barrier)
-      if (s.ph > 0 && !__all_sync(0xffffffffu, mbar_wait(go, (s.ph - 1) & 1, w))) break;
-      if (lane == 0) fence_proxy_async_global();
+      int waited = -1, arrive = 0;
       for (int u = first; ok && u < nunits; u += step, ++it) {
-        if (u != first) n = ns_unit<T>(p, s, u);
+        const NsUnit n = ns_unit<T>(p, s, u);
+        if (ns_need(p, s, n, waited) >= 0) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&go[waits & (kNsAhead - 1)], (waits / kNsAhead) & 1, w))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) fence_proxy_async_global();
+          ++waits;
+        }
         const int acc = it & 1;
         const uint32_t par = (it >> 1) & 1;
         if (s.f.kind == kNsSquare)
@@ -931,18 +974,24 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           else
             mbar_arrive(&tempty[acc]);
         }
+        if (!ok) break;
+        arrive += n.weight;
+        if (!p.few && u + step < nunits) continue;
+        // this warp's results of the unit (or of all its units of the phase) are in memory: arrive
+        if (lane == 0) {
+          bulk_wait_all<0>();
+          fence_proxy_async_global();
+        }
+        __syncwarp();
+        // the CTA's last warp arrives for all of them: its release covers what the
+        // others' lanes wrote before the warp barrier and their arrivals here
+        int* done = &warps_done[it & (kNsAhead - 1)];
+        if (lane == 0 && add_acq_rel_cta(done, 1) == kNsEpiWarps - 1) {
+          *done = 0;
+          red_release_add(p.counters + (p.few ? n.bz : 0), arrive);
+        }
+        arrive = 0;
       }
-      if (!ok) break;
-      // this warp's results of the phase are in memory: arrive
-      if (lane == 0) {
-        bulk_wait_all<0>();
-        fence_proxy_async_global();
-      }
-      __syncwarp();
-      // the CTA's last warp arrives for all of them: its release covers what the
-      // others' lanes wrote before the warp barrier and their arrivals here
-      if (lane == 0 && !s.last_phase() && add_acq_rel_cta(warps_done, 1) == kNsEpiWarps * (s.ph + 1) - 1)
-        red_release_add(p.counters, 1);
     }
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();

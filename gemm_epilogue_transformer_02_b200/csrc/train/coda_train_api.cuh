@@ -104,7 +104,11 @@ inline int norm8_bwd_blocks(int64_t M, int64_t N) {
 
 constexpr int kNsMaxNormBlocks = 1184;  // eight for each of 148 SMs
 
-constexpr int kNsMaxCounters = 1 + kGeos * kNsSplitCounters;
+// With up to this many units for each CTA (or pair) in the longest phase each unit
+// waits for its own matrix (ns_kernel has the figures).
+constexpr int kNsFew = 4;
+
+inline int ns_counters(int64_t batch) { return static_cast<int>(batch) + kGeos * kNsSplitCounters; }
 
 struct NsPlan {
   int64_t batch, m, n, s;  // s: the smaller side
@@ -158,7 +162,7 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
     p.diag[i] = take(used ? static_cast<size_t>(batch) * p.s * 8 : 0);
   }
   p.sums = take(static_cast<size_t>(batch) * p.norm_blocks * 8);
-  p.counters = take(kNsMaxCounters * 4);
+  p.counters = take(static_cast<size_t>(ns_counters(batch)) * 4);
   // at most one split unit per CTA (pair) of the grid
   p.part = take(p.tile == 64 ? 0 : static_cast<size_t>(148) * 128 * p.tile * 4);
   p.bytes = o;
@@ -208,6 +212,8 @@ NsGeo ns_geo(int64_t batch, int64_t rows, int64_t cols, int64_t K, bool sym, int
   while (g.rest > 0 && 2 * g.splits <= tile / 64 && 2 * g.splits * g.rest <= slots &&
          g.nkb / (2 * g.splits) >= 8)
     g.splits *= 2;
+  // of each CTA at each of a matrix's tiles, a whole one as often as a split one
+  g.arrivals = g.tiles * g.splits * (tile == 256 ? 2 : 1);
   return g;
 }
 
@@ -248,9 +254,14 @@ coda_status_t ns_launch(int dev, DevInfo* info, NsParams& p, const NsPlan& pl, c
   p.geo[kGeoGram] = ns_geo(pl.batch, s, s, l, true, N, slots[dev]);
   p.geo[kGeoSym] = ns_geo(pl.batch, s, s, s, true, N, slots[dev]);
   p.geo[kGeoSym2] = ns_geo(2 * pl.batch, s, s, s, true, N, slots[dev]);
+  p.geo[kGeoSym2].arrivals *= 2;  // two products of a matrix
   p.geo[kGeoUpdate] = ns_geo(pl.batch, pl.m, pl.n, s, false, N, slots[dev]);
-  int n = 0;
-  for (const NsGeo& g : p.geo) n = std::max(n, g.whole > 0 ? slots[dev] : g.rest * g.splits);
+  int n = 0, units = 0;
+  for (const NsGeo& g : p.geo) {
+    n = std::max(n, g.whole > 0 ? slots[dev] : g.rest * g.splits);
+    if (pl.grouped || &g != &p.geo[kGeoSym2]) units = std::max(units, g.whole + g.rest * g.splits);
+  }
+  p.few = pl.batch > 1 && units <= kNsFew * slots[dev];
   p.wait_ns = static_cast<uint64_t>(g_wait_ns);
   cfg.gridDim = dim3(static_cast<unsigned>(PAIR ? 2 * n : n), 1, 1);
   cfg.stream = stream;
@@ -503,7 +514,7 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
   st = launch_pdl(ns_scale_kernel, dim3(static_cast<unsigned>(pl.norm_blocks), static_cast<unsigned>(batch)),
                   kNsNormThreads, 0, 0, stm, G, n8, pl.norm_blocks, static_cast<const double*>(sums),
                   static_cast<double>(eps), hi[0], lo[0], p.counters,
-                  kNsMaxCounters);
+                  ns_counters(batch));
   if (st != CODA_OK) return st;
   if (pl.tile == 256) return ns_launch<256>(dev, info, p, pl, stm);
   return pl.tile == 128 ? ns_launch<128>(dev, info, p, pl, stm) : ns_launch<64>(dev, info, p, pl, stm);
