@@ -45,6 +45,9 @@ inline int embed_chunk(int64_t M) {
   return static_cast<int>(c);
 }
 
+// The sort counts rows in ints, up to 1023 past the last.
+constexpr int64_t kEmbBwdMaxRows = kMaxInt - 1023;
+
 struct EmbedWs {
   size_t buf0, buf1, part, list, crossing, bitmap, words, bytes;
   int chunk, items;
@@ -109,6 +112,12 @@ constexpr int kNsMaxNormBlocks = 1184;  // eight for each of 148 SMs
 constexpr int kNsFew = 4;
 
 inline int ns_counters(int64_t batch) { return static_cast<int>(batch) + kGeos * kNsSplitCounters; }
+
+// (byte strides of the tensor maps; tiles are counted in ints)
+inline bool ns_shape_ok(int64_t batch, int64_t m, int64_t n) {
+  return batch >= 0 && batch <= 65535 && dim_ok(m) && dim_ok(n) && m * n <= int64_t(1) << 38 &&
+         2 * batch * ((m + 127) / 128) * ((n + 63) / 64) <= kMaxInt;
+}
 
 struct NsPlan {
   int64_t batch, m, n, s;  // s: the smaller side
@@ -296,13 +305,13 @@ coda_status_t coda_embed(const int64_t* tokens, const uint16_t* E, float scale, 
 }
 
 size_t coda_embed_bwd_workspace_size(int64_t M, int64_t D, int64_t V) {
-  if (M <= 0 || M > kMaxInt || !dim_ok(D) || V <= 0 || V >= kMaxInt) return 0;
+  if (M <= 0 || M > kEmbBwdMaxRows || !dim_ok(D) || V <= 0 || V >= kMaxInt) return 0;
   return embed_ws(M, D, V).bytes;
 }
 
 coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float scale, float* dE, int accumulate, void* ws,
                              size_t ws_bytes, int64_t M, int64_t D, int64_t V, void* stream) {
-  CODA_CHECK(M >= 0 && M <= kMaxInt && dim_ok(D) && V > 0 && V < kMaxInt, CODA_ERR_SHAPE);
+  CODA_CHECK(M >= 0 && M <= kEmbBwdMaxRows && dim_ok(D) && V > 0 && V < kMaxInt, CODA_ERR_SHAPE);
   CODA_CHECK(dE && (M == 0 || (tokens && dh)), CODA_ERR_NULL);
   CODA_CHECK(al16(tokens) && al16(dh) && al16(dE) && al16(ws), CODA_ERR_ALIGN);
   CODA_CHECK(M == 0 || (ws && ws_bytes >= embed_ws(M, D, V).bytes), CODA_ERR_WORKSPACE);
@@ -459,21 +468,18 @@ coda_status_t coda_add_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const 
 }
 
 size_t coda_newton_schulz_workspace_size(int64_t batch, int64_t m, int64_t n) {
-  if (batch <= 0 || !dim_ok(m) || !dim_ok(n)) return 0;
+  if (batch <= 0 || !ns_shape_ok(batch, m, n)) return 0;
   return ns_plan(batch, m, n).bytes;
 }
 
 coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, int64_t m, int64_t n, int steps, float a,
                                  float b, float c, float eps, void* ws, size_t ws_bytes, void* stream) {
-  CODA_CHECK(batch >= 0 && batch <= 65535 && dim_ok(m) && dim_ok(n) && steps >= 1 && steps <= 100 && eps >= 0.f,
-             CODA_ERR_SHAPE);
-  CODA_CHECK(m * n <= int64_t(1) << 38, CODA_ERR_SHAPE);  // byte strides of the tensor maps
+  CODA_CHECK(ns_shape_ok(batch, m, n) && steps >= 1 && steps <= 100 && eps >= 0.f, CODA_ERR_SHAPE);
   if (batch == 0) return CODA_OK;
   CODA_CHECK(G && out, CODA_ERR_NULL);
   CODA_CHECK(al16(G) && al16(out) && al16(ws), CODA_ERR_ALIGN);
   const NsPlan pl = ns_plan(batch, m, n);
   CODA_CHECK(ws && ws_bytes >= pl.bytes, CODA_ERR_WORKSPACE);
-  CODA_CHECK(2 * batch * ((m + 127) / 128) * ((n + 63) / 64) <= kMaxInt, CODA_ERR_SHAPE);
   int dev;
   DevInfo* info;
   coda_status_t st = current_device(&dev, &info);

@@ -516,7 +516,7 @@ size_t coda_embed_bwd_workspace_size(int64_t M, int64_t D, int64_t V);
  * of dE is written (zero where the token does not occur); accumulate != 0: the
  * sums are added to dE, whose other rows are not touched.  Tokens outside
  * [0, V) contribute nothing.  dh [M, D] bf16, dE [V, D] fp32.  M == 0 zeroes
- * dE or, accumulating, does nothing. */
+ * dE or, accumulating, does nothing.  M at most 2^31 - 1024. */
 coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float scale, float* dE, int accumulate, void* ws,
                              size_t ws_bytes, int64_t M, int64_t D, int64_t V, void* stream);
 
@@ -554,7 +554,7 @@ coda_status_t coda_add_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const 
                                    size_t ws_bytes, int64_t M, int64_t N, void* stream);
 
 /* Bytes of workspace coda_newton_schulz needs (0 for a bad shape): X twice in
- * two fp16 parts, and two square fp16 matrices of the smaller side. */
+ * two fp16 parts, and two to five square fp16 matrices of the smaller side. */
 size_t coda_newton_schulz_workspace_size(int64_t batch, int64_t m, int64_t n);
 
 /* Newton-Schulz orthogonalisation of `batch` matrices (the step of the Muon

@@ -52,7 +52,9 @@ def test_embed_bwd_refusals(lib):
     assert f(None, Q, 1.0, R, 0, S, n, 4, 64, 10, None) == NULL
     assert f(P, None, 1.0, R, 0, S, n, 4, 64, 10, None) == NULL
     assert f(P, Q, 1.0, None, 0, S, n, 4, 64, 10, None) == NULL
-    for M, D, V in ((-1, 64, 10), (4, 60, 10), (4, 64, 0), (4, 64, (1 << 31) - 1)):
+    last = (1 << 31) - 1024  # the sort's row numbers stay in 32 bits
+    assert size(last, 8, 10) > 16 * last and size(last + 1, 8, 10) == 0
+    for M, D, V in ((-1, 64, 10), (4, 60, 10), (4, 64, 0), (4, 64, (1 << 31) - 1), (last + 1, 8, 10)):
         assert f(P, Q, 1.0, R, 0, S, BIG, M, D, V, None) == SHAPE
     for i in (0, 1, 3, 5):
         a = [P, Q, 1.0, R, 0, S]
@@ -115,6 +117,7 @@ def test_newton_schulz_refusals(lib):
     n = size(2, 64, 128)
     assert n >= 2 * (4 * 64 * 128 + 2 * 64 * 64) * 2
     assert size(0, 64, 64) == 0 and size(1, 60, 64) == 0 and size(1, 64, 0) == 0
+    assert size(65536, 64, 64) == 0 and size(1, 1 << 20, 1 << 20) == 0
     c = (3.4445, -4.775, 2.0315)
     assert f(P, Q, 0, 64, 128, 5, *c, 1e-7, None, 0, None) == OK
     assert f(P, Q, 2, 64, 128, 5, *c, 1e-7, R, n - 1, None) == WS
