@@ -135,22 +135,24 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
   p.n = n;
   p.tall = m > n;
   p.s = p.tall ? n : m;
-  // CTA pairs (half of the operand traffic) where K is long and their 256 x 256
-  // tiles fill more than one round of the 74 pairs: 333 against 434 us for two of
-  // 2048 x 2048, 1040 against 1420 at 4096 x 4096.  With fewer tiles or a short K
-  // the four times as many small ones end sooner: 171 against 213 us at 1024 x
-  // 4096, 269 against 311 for eight of 1024 x 1024, 245 against 249 at 2048 x
-  // 2048; 512 tiles of K 1024 425 against 458 us, 256 of them 311 against 290.
-  // The smallest where all of them run at once: 94 against 113 us at 512 x
-  // 512, 73 against 91 at 256 x 256.
+  // CTA pairs (half of the operand traffic) where their 256 x 256 tiles fill more
+  // than one round of the 74 pairs: with a long K those of X (323 against 385 us
+  // for two of 2048 x 2048, 591 against 790 for four, 1050 against 1500 at 4096 x
+  // 4096), with a shorter one those of the square matrices too, whose phases are
+  // most of a step (313 against 389 for twelve of 1024 x 1024, 437 against 493 for
+  // sixteen), or several rounds of X's (425 against 458 at 1024 x 32768).  With
+  // fewer the four times as many small ones end sooner: 201 against 265 at 1024 x
+  // 4096, 312 against 377 for four of them; eight of 1024 x 1024 (240) and 2048 x
+  // 2048 (251) are equal.  The smallest where all of them run at once: 94 against
+  // 113 us at 512 x 512, 73 against 91 at 256 x 256.
   const int64_t t256 = batch * ((m + 255) / 256) * ((n + 255) / 256);
-  p.tile = t256 >= (p.s >= 1536 ? 100 : 400) && p.s >= 1024        ? 256
-           : batch * ((m + 127) / 128) * ((n + 63) / 64) <= 148 ? 64
-                                                                : 128;
+  const int64_t s256 = (p.s + 255) / 256, square = batch * s256 * s256;
+  const bool pairs = p.s >= 1536 ? t256 >= 100 : p.s >= 1024 && (square >= 150 || t256 >= 400);
+  p.tile = pairs ? 256 : batch * ((m + 127) / 128) * ((n + 63) / 64) <= 148 ? 64 : 128;
   // Groups save 9 s^2 l operations of five steps and cost 9 s^3 and two more
-  // phases: 650 against 1060 us at 2048 x 16384, 298 against 367 at 2048 x 4096,
-  // 164 against 173 at 1024 x 2560, but 152 against 148 at 1024 x 2048 and 267
-  // against 249 at 2048 x 2048.  Below 512 they would save little and cost
+  // phases: 626 against 984 us at 2048 x 16384, 298 against 367 at 2048 x 4096,
+  // 164 against 173 at 1024 x 2560, but 152 against 148 at 1024 x 2048 and 253
+  // against 251 at 2048 x 2048.  Below 512 they would save little and cost
   // accuracy (2.6e-3 against 2.0e-3 of |X|_F, the output's rounding included).
   p.grouped = p.s >= 512 && (p.tall ? m : n) >= 2 * p.s;
   const int64_t n8 = m * n / 8;

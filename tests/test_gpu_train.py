@@ -384,6 +384,21 @@ def test_newton_schulz(m, n, batch):
     assert torch.equal(C.newton_schulz(G), out.t)
 
 
+@pytest.mark.parametrize("batch,m,n", [(2, 8, 8), (40, 72, 136), (5, 520, 512), (16, 512, 512), (90, 264, 256),
+                                       (600, 64, 64), (12, 1032, 1024), (5, 1032, 2072), (3, 1544, 1640)])
+def test_newton_schulz_batches(batch, m, n):
+    """Matrices go from phase to phase by themselves where there are few tiles,
+    and together where there are many; each is what it is alone, in every run."""
+    G = randn(gen(batch), batch, m, n)
+    G[batch // 2, m // 2, n // 3] = float("nan")
+    out = C.newton_schulz(G)
+    assert not out[batch // 2].isfinite().any()
+    keep = torch.arange(batch, device="cuda") != batch // 2
+    ns_check(out[keep], G[keep])
+    for _ in range(3):
+        assert torch.equal(C.newton_schulz(G)[keep], out[keep])
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 7])
 def test_newton_schulz_steps(steps):
     G = randn(gen(steps), 200, 328)
