@@ -8,7 +8,7 @@
 //
 // Each element is read once and each output written once; both are bound by
 // HBM (7 and 8 bytes an element).  A row lives in the registers of one block
-// from its load to its store: sums, r and y are fp32, h and dx are rounded to
+// or warp from its load to its store: sums, r and y are fp32, h and dx are rounded to
 // bf16 once.
 #pragma once
 
@@ -16,12 +16,13 @@
 
 namespace coda {
 
-// Sum over the block; every thread gets it.  `red` holds 32 floats; the caller
-// synchronises before its next use.
-__device__ __forceinline__ float norm8_block_sum(float s, float* red) {
+// Sum over the row's threads, a warp or the block; every one gets it.  `red`
+// holds 32 floats; the caller synchronises before its next use.
+template <bool WARP>
+__device__ __forceinline__ float norm8_sum(float s, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (blockDim.x == 32) return s;
+  if (WARP || blockDim.x == 32) return s;
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
   s = red[threadIdx.x & 31];  // entries past the block's warps are zero
@@ -30,35 +31,40 @@ __device__ __forceinline__ float norm8_block_sum(float s, float* red) {
   return s;
 }
 
-// One block per row; thread t holds the 8-column vectors t, t + blockDim, ...
-// (VPT of them).  MX: four neighbouring threads hold a 32-column block, sixteen
-// the four blocks whose scale bytes make one word of the A layout; rows from M
-// up to a whole 128-row block only write their scale bytes (127).
+// One block per row, or (WARP) a warp; its thread t holds the 8-column vectors
+// t and t + threads.  MX: four neighbouring threads hold a 32-column block,
+// sixteen the four blocks whose scale bytes make one word of the A layout; rows
+// from M up to a whole 128-row block only write their scale bytes (127).
 // !MX: codes of y / s_y; amax = max |y| by atomic max on its bits (the order of
 // a maximum does not matter), or a plain store where one block is all.
-template <bool MX, int VPT>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(
+constexpr int kNorm8Vpt = 2;
+
+template <bool MX, bool WARP, int MAXT, int BLOCKS>
+__global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_kernel(
     const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ res,
     const __nv_bfloat16* __restrict__ gamma, float eps, const float* __restrict__ s_y,
     __nv_bfloat16* __restrict__ h_out, uint8_t* __restrict__ q, uint8_t* __restrict__ sf, unsigned* amax,
     float* __restrict__ r_out, int64_t M, int N, int nrb) {
+  constexpr int VPT = kNorm8Vpt;
   __shared__ float red[32];
   __shared__ unsigned mred[32];
   pdl_begin();
-  const int64_t row = blockIdx.x;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   if (MX && row >= M) {
-    for (int j = threadIdx.x; j < N / 128; j += blockDim.x)
+    for (int j = tid; j < N / 128; j += nt)
       *reinterpret_cast<uint32_t*>(sf + mx_sf_offset_a(static_cast<int>(row), 4 * j, nrb)) = 0x7f7f7f7fu;
     return;
   }
-  if (threadIdx.x < 32) red[threadIdx.x] = 0.f;
+  if (!WARP && tid < 32) red[tid] = 0.f;
+  const int cols = row < M ? N : 0;  // (past the last row a warp only takes part in the maximum)
   const size_t ro = static_cast<size_t>(row) * N;
   uint4 xv[VPT], rv[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int c = (threadIdx.x + k * blockDim.x) * 8;
+    const int c = (tid + k * nt) * 8;
     xv[k] = rv[k] = make_uint4(0, 0, 0, 0);
-    if (c < N) {
+    if (c < cols) {
       xv[k] = __ldcs(reinterpret_cast<const uint4*>(x + ro + c));
       if (res != nullptr) rv[k] = __ldcs(reinterpret_cast<const uint4*>(res + ro + c));
     }
@@ -66,10 +72,10 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(
   uint4 gv[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int c = (threadIdx.x + k * blockDim.x) * 8;
-    gv[k] = c < N ? __ldg(reinterpret_cast<const uint4*>(gamma + c)) : make_uint4(0, 0, 0, 0);
+    const int c = (tid + k * nt) * 8;
+    gv[k] = c < cols ? __ldg(reinterpret_cast<const uint4*>(gamma + c)) : make_uint4(0, 0, 0, 0);
   }
-  if (blockDim.x > 32) __syncthreads();  // `red` is cleared
+  if (!WARP && nt > 32) __syncthreads();  // `red` is cleared
   float h[VPT][8];
   float ss = 0.f;
 #pragma unroll
@@ -86,16 +92,16 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(
       ss = fmaf(b, b, ss);
       o[e] = pack_bf16x2(a, b);
     }
-    const int c = (threadIdx.x + k * blockDim.x) * 8;
-    if (h_out != nullptr && c < N) *reinterpret_cast<uint4*>(h_out + ro + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    const int c = (tid + k * nt) * 8;
+    if (h_out != nullptr && c < cols) *reinterpret_cast<uint4*>(h_out + ro + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
-  const float r = rsqrtf(norm8_block_sum(ss, red) / static_cast<float>(N) + eps);
-  if (threadIdx.x == 0 && r_out != nullptr) r_out[row] = r;
+  const float r = rsqrtf(norm8_sum<WARP>(ss, red) / static_cast<float>(N) + eps);
+  if (tid == 0 && cols > 0 && r_out != nullptr) r_out[row] = r;
   const float inv = MX ? 0.f : 1.0f / __ldg(s_y);
   float am = 0.f;
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int c = (threadIdx.x + k * blockDim.x) * 8;
+    const int c = (tid + k * nt) * 8;
     const uint32_t gw[4] = {gv[k].x, gv[k].y, gv[k].z, gv[k].w};
     float y[8];
     float bm = 0.f;
@@ -114,14 +120,14 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(
       uint32_t word = static_cast<uint32_t>(e + 127) << (8 * ((threadIdx.x >> 2) & 3));
       word |= __shfl_xor_sync(0xffffffffu, word, 4);
       word |= __shfl_xor_sync(0xffffffffu, word, 8);
-      if ((threadIdx.x & 15) == 0 && c < N)
+      if ((threadIdx.x & 15) == 0 && c < cols)
         *reinterpret_cast<uint32_t*>(sf + mx_sf_offset_a(static_cast<int>(row), c >> 5, nrb)) = word;
     } else {
       am = fmaxf(am, bm);
     }
     const uint32_t q0 = pack_e4m3x2(y[0] * f, y[1] * f) | (pack_e4m3x2(y[2] * f, y[3] * f) << 16);
     const uint32_t q1 = pack_e4m3x2(y[4] * f, y[5] * f) | (pack_e4m3x2(y[6] * f, y[7] * f) << 16);
-    if (c < N) *reinterpret_cast<uint2*>(q + ro + c) = make_uint2(q0, q1);
+    if (c < cols) *reinterpret_cast<uint2*>(q + ro + c) = make_uint2(q0, q1);
   }
   if (!MX) {
     unsigned u = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
@@ -140,7 +146,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(
   }
 }
 
-// A block walks rows blockIdx, + gridDim, ...; the next row's vectors are
+// A block (WARP: a warp) walks rows blockIdx, + gridDim, ...; the next row's vectors are
 // requested before this row's sum is reduced (not with more than 512 threads,
 // whose 64 registers do not hold both rows).  dgamma's terms stay in registers
 // over the block's rows; the blocks' sums part[block][N] are added up by
@@ -148,22 +154,26 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(
 // of them hide each other's reductions until their registers no longer hold both
 // rows (8192 x 2048, 128 threads: 4 blocks 28.8 us, 5 24.7, 6 32.4; bulk copies
 // into a ring of shared memory 45, two rows ahead 29.3).
-template <int VPT, int MAXT, int BLOCKS>
+template <bool WARP, int MAXT, int BLOCKS>
 __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ h, const float* __restrict__ r,
     const __nv_bfloat16* __restrict__ gamma, const __nv_bfloat16* __restrict__ d_h, __nv_bfloat16* __restrict__ dx,
     float* __restrict__ part, int64_t M, int N) {
+  constexpr int VPT = kNorm8Vpt;
   constexpr bool kAhead = MAXT <= 512;
   __shared__ float red[2][32];
   pdl_begin();
-  if (threadIdx.x < 32) red[0][threadIdx.x] = red[1][threadIdx.x] = 0.f;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+  const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * (MAXT / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * (MAXT / 32) : gridDim.x;
+  if (!WARP && tid < 32) red[0][tid] = red[1][tid] = 0.f;
   uint4 yv[VPT], hv[VPT], sv[VPT];
   float dg[VPT][8];
   const auto load = [&](int64_t row) {
     const size_t ro = static_cast<size_t>(row) * N;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int c = (threadIdx.x + k * blockDim.x) * 8;
+      const int c = (tid + k * nt) * 8;
       yv[k] = hv[k] = sv[k] = make_uint4(0, 0, 0, 0);
       if (c < N && row < M) {
         yv[k] = __ldcs(reinterpret_cast<const uint4*>(dy + ro + c));
@@ -173,17 +183,17 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_bwd_kernel(
     }
   };
   const auto gamma_of = [&](int k) {  // (from L1: registers hold the rows in flight)
-    const int c = (threadIdx.x + k * blockDim.x) * 8;
+    const int c = (tid + k * nt) * 8;
     return c < N ? __ldg(reinterpret_cast<const uint4*>(gamma + c)) : make_uint4(0, 0, 0, 0);
   };
-  if (kAhead) load(blockIdx.x);
+  if (kAhead) load(first);
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[k][e] = 0.f;
-  if (blockDim.x > 32) __syncthreads();
+  if (!WARP && nt > 32) __syncthreads();
   int it = 0;
-  for (int64_t row = blockIdx.x; row < M; row += gridDim.x, it ^= 1) {
+  for (int64_t row = first; row < M; row += step, it ^= 1) {
     if (!kAhead) load(row);
     uint4 y0[VPT], h0[VPT], s0[VPT];
     float s = 0.f;
@@ -202,12 +212,12 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_bwd_kernel(
       }
     }
     const float ri = __ldg(r + row);
-    if (kAhead) load(row + gridDim.x);
-    const float coef = -ri * ri * ri * norm8_block_sum(s, red[it]) / static_cast<float>(N);
+    if (kAhead) load(row + step);
+    const float coef = -ri * ri * ri * norm8_sum<WARP>(s, red[it]) / static_cast<float>(N);
     const size_t ro = static_cast<size_t>(row) * N;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int c = (threadIdx.x + k * blockDim.x) * 8;
+      const int c = (tid + k * nt) * 8;
       const uint4 g = gamma_of(k);
       const uint32_t yw[4] = {y0[k].x, y0[k].y, y0[k].z, y0[k].w}, hw[4] = {h0[k].x, h0[k].y, h0[k].z, h0[k].w};
       const uint32_t sw[4] = {s0[k].x, s0[k].y, s0[k].z, s0[k].w}, gw[4] = {g.x, g.y, g.z, g.w};
@@ -224,9 +234,28 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_bwd_kernel(
       if (c < N) *reinterpret_cast<uint4*>(dx + ro + c) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
+  if (WARP) {
+    // the warps' terms, added in order by the first
+    __shared__ float terms[MAXT / 32 - 1][8 * kNorm8Vpt][32];
+    const int warp = threadIdx.x >> 5;
+    if (warp > 0) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) terms[warp - 1][k * 8 + e][tid] = dg[k][e];
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 0; w < MAXT / 32 - 1; ++w)
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dg[k][e] += terms[w][k * 8 + e][tid];
+  }
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int c = (threadIdx.x + k * blockDim.x) * 8;
+    const int c = (tid + k * nt) * 8;
     if (c < N) {
       float* o = part + static_cast<size_t>(blockIdx.x) * N + c;
       *reinterpret_cast<float4*>(o) = make_float4(dg[k][0], dg[k][1], dg[k][2], dg[k][3]);

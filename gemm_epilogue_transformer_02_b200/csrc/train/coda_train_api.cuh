@@ -74,33 +74,44 @@ inline size_t embed_zero_first(int64_t M) { return (size_t(48) << 20) + static_c
 
 // --------------------------------------------------------------------- norm
 
-// A row's block: two 8-column vectors a thread (one for rows of up to 512), so
-// a row of up to 16384 columns stays in one block's registers.
+// Two 8-column vectors a thread, so a row of up to 16384 columns stays in one
+// block's registers.  Narrow rows have a warp each, four to a block: as blocks of
+// 64 threads they were bound by the rate at which blocks start and by their
+// barriers (MXFP8, 32768 x 128 34.2 us against 14.1, 16384 x 512 17.7 against
+// 11.6; but 1024 columns, four vectors a lane, 12.8 against 11.8 as blocks).
 constexpr int64_t kNorm8MaxN = 16384;
-inline int norm8_vpt(int64_t N) { return N <= 512 ? 1 : 2; }
-inline int norm8_threads(int64_t N) {
-  const int64_t t = (N / 8 + norm8_vpt(N) - 1) / norm8_vpt(N);
-  return static_cast<int>((t + 31) & ~int64_t(31));
-}
+constexpr int64_t kNorm8WarpN = 512;
+constexpr int kNorm8WarpThreads = 128;
+inline int norm8_threads(int64_t N) { return static_cast<int>(((N / 8 + 1) / 2 + 31) & ~int64_t(31)); }
 
 template <bool MX>
 coda_status_t launch_norm8(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float eps, const float* s_y,
                            uint16_t* h_out, uint8_t* q, uint8_t* sf, unsigned* amax, float* r_out, int64_t M,
                            int64_t N, cudaStream_t s) {
-  const int64_t nrb = (M + 127) / 128;
-  auto kern = norm8_vpt(N) == 1 ? add_rmsnorm_kernel<MX, 1> : add_rmsnorm_kernel<MX, 2>;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(MX ? nrb * 128 : M)), norm8_threads(N), 0, 0, s,
+  const int64_t nrb = (M + 127) / 128, rows = MX ? nrb * 128 : M;
+  const bool warp = N <= kNorm8WarpN;
+  const int threads = warp ? static_cast<int>(std::min<int64_t>(kNorm8WarpThreads, 32 * rows)) : norm8_threads(N);
+  const int64_t blocks = warp ? (rows + threads / 32 - 1) / (threads / 32) : rows;
+  if (!MX && blocks > 1 && cudaMemsetAsync(amax, 0, sizeof(float), s) != cudaSuccess) return CODA_ERR_LAUNCH;
+  // (registers for as many blocks as hide each other's reductions: 4096 x 8192
+  // 41.3 us against 47.5 with two of 512 threads, 2048 x 16384 45.1 against 55.0)
+  auto kern = warp             ? add_rmsnorm_kernel<MX, true, kNorm8WarpThreads, 1>
+              : threads <= 256 ? add_rmsnorm_kernel<MX, false, 256, 5>
+              : threads <= 512 ? add_rmsnorm_kernel<MX, false, 512, 4>
+                               : add_rmsnorm_kernel<MX, false, 1024, 2>;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), threads, 0, 0, s,
                     reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(res),
                     reinterpret_cast<const __nv_bfloat16*>(gamma), eps, s_y, reinterpret_cast<__nv_bfloat16*>(h_out),
                     q, sf, amax, r_out, M, static_cast<int>(N), static_cast<int>(nrb));
 }
 
 // Blocks of the norm's backward: as many as 148 SMs hold at once, so that every
-// block has as many rows.
+// block has as many rows (narrow rows, a warp each: 16384 x 512 17.2 us, five
+// blocks 19.3, a block of 64 threads each 22.0).
 inline int norm8_bwd_blocks(int64_t M, int64_t N) {
+  if (N <= kNorm8WarpN) return static_cast<int>(std::min<int64_t>((M + 3) / 4, 148 * 4));
   const int t = norm8_threads(N);
-  const int64_t per_sm = t <= 64 ? 640 / t : (t <= 128 ? 5 : (t <= 256 ? 2 : 1));
-  return static_cast<int>(std::min<int64_t>(M, 148 * per_sm));
+  return static_cast<int>(std::min<int64_t>(M, 148 * (t <= 128 ? 640 / t : (t <= 256 ? 2 : 1))));
 }
 
 // ------------------------------------------------------------ Newton-Schulz
@@ -427,7 +438,6 @@ coda_status_t coda_add_rmsnorm_fp8(const uint16_t* x, const uint16_t* res, const
   const coda_status_t st = current_device(&dev, &info);
   if (st != CODA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (M > 1 && cudaMemsetAsync(amax_out, 0, sizeof(float), s) != cudaSuccess) return CODA_ERR_LAUNCH;
   return launch_norm8<false>(x, res, gamma, eps, s_y, h_out, y8_out, nullptr, reinterpret_cast<unsigned*>(amax_out),
                              r_out, M, N, s);
 }
@@ -454,12 +464,12 @@ coda_status_t coda_add_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const 
   if (M == 0)
     return cudaMemsetAsync(dgamma_out, 0, static_cast<size_t>(N) * 4, s) == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
   const int blocks = norm8_bwd_blocks(M, N);
-  const int threads = norm8_threads(N);
-  auto kern = norm8_vpt(N) == 1 ? add_rmsnorm_bwd_kernel<1, 64, 10>
-                                : (threads <= 128   ? add_rmsnorm_bwd_kernel<2, 128, 5>
-                                   : threads <= 256 ? add_rmsnorm_bwd_kernel<2, 256, 2>
-                                   : threads <= 512 ? add_rmsnorm_bwd_kernel<2, 512, 1>
-                                                    : add_rmsnorm_bwd_kernel<2, 1024, 1>);
+  const int threads = N <= kNorm8WarpN ? kNorm8WarpThreads : norm8_threads(N);
+  auto kern = N <= kNorm8WarpN ? add_rmsnorm_bwd_kernel<true, kNorm8WarpThreads, 4>
+                               : (threads <= 128   ? add_rmsnorm_bwd_kernel<false, 128, 5>
+                                  : threads <= 256 ? add_rmsnorm_bwd_kernel<false, 256, 2>
+                                  : threads <= 512 ? add_rmsnorm_bwd_kernel<false, 512, 1>
+                                                   : add_rmsnorm_bwd_kernel<false, 1024, 1>);
   st = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), threads, 0, 0, s,
                   reinterpret_cast<const __nv_bfloat16*>(dy), reinterpret_cast<const __nv_bfloat16*>(h), r,
                   reinterpret_cast<const __nv_bfloat16*>(gamma), reinterpret_cast<const __nv_bfloat16*>(d_h),

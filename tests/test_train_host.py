@@ -95,7 +95,7 @@ def test_norm_refusals(lib):
 def test_norm_bwd_refusals(lib):
     f, size = lib.coda_add_rmsnorm_bwd, lib.coda_add_rmsnorm_bwd_workspace_size
     n = size(5, 64)
-    assert n == 5 * 64 * 4 and size(0, 64) == 0 and size(5, 60) == 0
+    assert 64 * 4 <= n <= 5 * 64 * 4 and size(0, 64) == 0 and size(5, 60) == 0
     assert size(1 << 20, 64) < 1 << 24  # the blocks, not the rows
     a0 = [P, Q, R, S, P, Q, R, S]
     assert f(*a0, n - 1, 5, 64, None) == WS
