@@ -146,21 +146,23 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_kernel(
   }
 }
 
-// A block (WARP: a warp) walks rows blockIdx, + gridDim, ...; the next row's vectors are
-// requested before this row's sum is reduced (not with more than 512 threads,
-// whose 64 registers do not hold both rows).  dgamma's terms stay in registers
-// over the block's rows; the blocks' sums part[block][N] are added up by
-// norm8_dgamma_kernel in a fixed order.  BLOCKS: of MAXT threads on an SM; more
-// of them hide each other's reductions until their registers no longer hold both
-// rows (8192 x 2048, 128 threads: 4 blocks 28.8 us, 5 24.7, 6 32.4; bulk copies
-// into a ring of shared memory 45, two rows ahead 29.3).
+// A block (WARP: a warp) walks rows blockIdx, + gridDim, ...  dgamma's terms stay
+// in registers over the block's rows; the blocks' sums part[block][N] are added up
+// by norm8_dgamma_kernel in a fixed order.  What bounds it is how much is in
+// flight.  Up to 128 threads (2048 columns) the next row's vectors are requested
+// before this row's sum is reduced, in as many blocks (BLOCKS of MAXT threads on
+// an SM) as have registers for both rows: 8192 x 2048 with 4 blocks 28.8 us, 5
+// 24.7, 6 32.4, without the next row and 8 blocks 27.5; bulk copies into a ring
+// of shared memory 45, two rows ahead 29.3.  Wider rows are better off with twice
+// the blocks and one row each (with norm8_dgamma_kernel, 8192 x 4096: 50.3 us
+// against 59.0, 4096 x 4104 32.0 against 50.5, 4096 x 8192 51.1 against 66.3).
 template <bool WARP, int MAXT, int BLOCKS>
 __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ h, const float* __restrict__ r,
     const __nv_bfloat16* __restrict__ gamma, const __nv_bfloat16* __restrict__ d_h, __nv_bfloat16* __restrict__ dx,
     float* __restrict__ part, int64_t M, int N) {
   constexpr int VPT = kNorm8Vpt;
-  constexpr bool kAhead = MAXT <= 512;
+  constexpr bool kAhead = MAXT <= 128;
   __shared__ float red[2][32];
   pdl_begin();
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;

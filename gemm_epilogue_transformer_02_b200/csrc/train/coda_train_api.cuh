@@ -111,7 +111,7 @@ coda_status_t launch_norm8(const uint16_t* x, const uint16_t* res, const uint16_
 inline int norm8_bwd_blocks(int64_t M, int64_t N) {
   if (N <= kNorm8WarpN) return static_cast<int>(std::min<int64_t>((M + 3) / 4, 148 * 4));
   const int t = norm8_threads(N);
-  return static_cast<int>(std::min<int64_t>(M, 148 * (t <= 128 ? 640 / t : (t <= 256 ? 2 : 1))));
+  return static_cast<int>(std::min<int64_t>(M, 148 * (t <= 128 ? 640 / t : t <= 512 ? 1024 / t : 1)));
 }
 
 // ------------------------------------------------------------ Newton-Schulz
@@ -467,8 +467,8 @@ coda_status_t coda_add_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const 
   const int threads = N <= kNorm8WarpN ? kNorm8WarpThreads : norm8_threads(N);
   auto kern = N <= kNorm8WarpN ? add_rmsnorm_bwd_kernel<true, kNorm8WarpThreads, 4>
                                : (threads <= 128   ? add_rmsnorm_bwd_kernel<false, 128, 5>
-                                  : threads <= 256 ? add_rmsnorm_bwd_kernel<false, 256, 2>
-                                  : threads <= 512 ? add_rmsnorm_bwd_kernel<false, 512, 1>
+                                  : threads <= 256 ? add_rmsnorm_bwd_kernel<false, 256, 4>
+                                  : threads <= 512 ? add_rmsnorm_bwd_kernel<false, 512, 2>
                                                    : add_rmsnorm_bwd_kernel<false, 1024, 1>);
   st = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), threads, 0, 0, s,
                   reinterpret_cast<const __nv_bfloat16*>(dy), reinterpret_cast<const __nv_bfloat16*>(h), r,

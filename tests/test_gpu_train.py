@@ -213,7 +213,8 @@ def y_err(N):
 
 
 @pytest.mark.parametrize("with_res", [True, False])
-@pytest.mark.parametrize("M,N", [(1, 128), (3, 384), (130, 512), (257, 2048), (20, 8192), (129, 640), (2, 16384)])
+@pytest.mark.parametrize("M,N", [(1, 128), (3, 384), (130, 512), (257, 2048), (20, 8192), (129, 640), (2, 16384),
+                                 (131, 128), (70, 4224), (5, 8320)])
 def test_add_rmsnorm_mx(M, N, with_res):
     x, res, gamma = norm_inputs(M, N, with_res, M + N)
     eps = 1e-6
@@ -243,7 +244,8 @@ def test_add_rmsnorm_mx(M, N, with_res):
 
 
 @pytest.mark.parametrize("with_res", [True, False])
-@pytest.mark.parametrize("M,N", [(1, 16), (1, 4096), (3, 528), (300, 512), (64, 2064), (9, 16384)])
+@pytest.mark.parametrize("M,N", [(1, 16), (1, 4096), (3, 528), (300, 512), (64, 2064), (9, 16384),
+                                 (2, 512), (301, 48), (6, 8208)])
 def test_add_rmsnorm_fp8(M, N, with_res):
     x, res, gamma = norm_inputs(M, N, with_res, M * 7 + N)
     eps = 1e-5
@@ -293,7 +295,8 @@ def test_norm8_keeps_a_bad_row_to_itself():
 
 
 @pytest.mark.parametrize("with_dh", [True, False])
-@pytest.mark.parametrize("M,N", [(1, 8), (5, 264), (257, 512), (130, 2048), (1500, 1032), (40, 8192), (7, 16384)])
+@pytest.mark.parametrize("M,N", [(1, 8), (5, 264), (257, 512), (130, 2048), (1500, 1032), (40, 8192), (7, 16384),
+                                 (5000, 40), (2401, 512), (1900, 2568), (700, 4104), (301, 8200)])
 def test_add_rmsnorm_bwd(M, N, with_dh):
     g = gen(M + 5 * N)
     h = (2 * randn(g, M, N)).to(BF)
