@@ -19,15 +19,13 @@
 // same shared memory, so the choice is one tensor map and two descriptor fields
 // per k-block.
 //
-// Groups of steps.  All A and P of a matrix are polynomials of its first A, so
-// they commute, and several steps can be taken on the small side alone:
-//   A' = P A P,  Q' = P' P,  and at the end of the group X' = Q X
-// (products of commuting symmetric matrices are symmetric: half of the work
-// again).  With s and l the smaller and larger side a step alone costs
-// 3 s^2 l + s^3 operations, five of them as groups of 3 and 2 cost 6 s^2 l +
-// 14 s^3 instead of 15 s^2 l + 5 s^3.  Rounding A' instead of forming X' X'^T
-// loses the smallest singular values sooner, so a group is at most three steps,
-// later ones two, and they are only used from s = 512 and l = 2 s on.
+// Every step forms A from X anew.  Several steps on the small side alone (A' =
+// P A P, X' = P' P X: all of them are polynomials of the first A) would save
+// s^2 l operations each, but A's rounding, relative to its large entries, then
+// stands for the small directions' share of the next steps: with one direction
+// in G and noise of 3e-4 beside it five steps as 3 + 2 ended 5e-2 of |X|_F off
+// (512 x 1024), 2 + 2 + 1 1e-2, a pair of steps at the end alone 4e-3, and
+// single ones 0.9e-3.
 //
 // Precision.  Operands are fp16, not bf16: with |X|_F = 1 every value is
 // bounded, so scaled by powers of two they use fp16's 11 bits where bf16 would
@@ -42,12 +40,13 @@
 //     rounding X put there.  X is therefore kept as a high and a low fp16 part;
 //     the GEMMs read the high part, and the diagonal of P (all of P where X is
 //     small) multiplies the low part too.  The last update drops it.
-// Against 64 bits this gives 0.3e-3 to 1.1e-3 of |X|_F for Gaussian and
-// correlated matrices after five steps.  Nearly low-rank ones (a few directions
-// hold the norm, the others grow by 3.4^5 from a hundredth of them) come to 1e-3
-// to 3e-3, in groups to 1e-2: there A's rounding, relative to its large entries,
-// grows with the small directions.  Plain bf16 products give 0.9e-2 and 3e-1.
-// The bf16 rounding of the output alone is 1.7e-3.
+// Against 64 bits this gives 0.2e-3 to 1.1e-3 of |X|_F for Gaussian and
+// correlated matrices after five steps (sides of 64 and more).  Where a few
+// directions hold the norm the others lie in the low part, which sees only P's
+// diagonal, and the entries of P beside it, of 2.7 / s for one direction, are
+// what is left out: with the smaller side s up to 1e-3 + 0.65 / s.  Plain bf16
+// products give 0.9e-2 and 3e-1.  The bf16 rounding of the output alone is
+// 1.7e-3.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -58,10 +57,10 @@ namespace coda {
 
 // Powers of two the fp16 values are stored with.  With the Muon coefficients
 // singular values stay below 1.3 and P below 3.5, so X fits with a factor of 12
-// to spare, A with 37, P and its products (at most 3.5^3) with 6.
+// to spare, A with 37, P with 73.
 constexpr float kNsScaleX = 4096.f;
-constexpr float kNsScaleA = 1024.f;  // A, P A
-constexpr float kNsScaleP = 256.f;   // P, Q
+constexpr float kNsScaleA = 1024.f;
+constexpr float kNsScaleP = 256.f;
 
 constexpr int kNsEpiWarps = 8;                     // two per TMEM lane quarter, each half of a tile's columns
 // Warps: loads of the left operand, MMA issue, epilogue, loads of the right
@@ -99,10 +98,10 @@ struct NsTile {
   static_assert(kSmem <= 232448, "shared memory");
 };
 
-enum NsKind : int { kNsGram = 0, kNsSquare, kNsMul, kNsUpdate };
+// The three phases of a step.
+enum NsKind : int { kNsGram = 0, kNsSquare, kNsUpdate, kNsKinds };
 
-// One GEMM's tiles, acc[i, j] = sum_k P[i, k] Q[j, k], over the batch (and over
-// two products, where a phase has two).
+// One GEMM's tiles, acc[i, j] = sum_k P[i, k] Q[j, k], over the batch.
 struct NsGeo {
   int rows, cols, nkb;    // output size of one matrix, 64-wide k-blocks
   int n_rt, n_ct, tiles;  // row tiles, column tiles, tiles of one matrix (half of them for a symmetric result)
@@ -111,10 +110,9 @@ struct NsGeo {
   int splits;             // are `splits` units each, over equal shares of the k-blocks
   int arrivals;           // at each matrix's counter in one such phase
 };
-enum NsGeoIndex : int { kGeoGram = 0, kGeoSym, kGeoSym2, kGeoUpdate, kGeos };
 
-// The symmetric matrices: A, P, P A, and the group's product Q (two, in turn).
-enum NsBuf : int { kBufA = 0, kBufP, kBufT, kBufQ0, kBufQ1, kBufs };
+// The symmetric matrices.
+enum NsBuf : int { kBufA = 0, kBufP, kBufs };
 
 // The loads of one matrix [batch, y, x], with 64-wide k-blocks.  A K-major
 // operand's 128 rows come as one copy: a single thread issues them, and at the
@@ -126,70 +124,36 @@ struct NsMaps {
 };
 
 struct NsParams {
-  NsMaps X[2];  // X's high part, by group parity
+  NsMaps X[2];  // X's high part, by the step's parity
   NsMaps S[kBufs];
   // the epilogues' boxes of 32 x 32 (64-byte swizzle): X's high and low parts, the symmetric matrices, the output
   CUtensorMap Hbox[2], Lbox[2], Sbox[kBufs], Obox;
   float2* diag[kBufs];  // [batch, s]: (d, f): what fp16 drops of the diagonal, and the rounded diagonal
   float* part;          // partial accumulators of the split tiles
   int* counters;        // [batch]: arrivals of finished units: of each matrix (if few), or of all at the first;
-                        // then for each geometry those of the split tiles' parts
-  NsGeo geo[kGeos];
+                        // then for each kind of phase those of the split tiles' parts
+  NsGeo geo[kNsKinds];
   int batch, steps, tall;
   int few;              // a unit waits for its own matrix (else for all of them)
-  int first, later;     // steps of the first group and of later ones, at most
   float a, b, c;
   uint64_t wait_ns;
 };
 
-// The phases of a group of one, two or three steps.  A matrix's phase begins when
-// its last one is complete.  A phase is a GEMM (or two products side by side: `two`) given by its
-// symmetric matrices: left, right, result.
-struct NsPhase {
-  uint8_t kind, two;
-  uint8_t l, r, out;
-  uint8_t l2, r2, out2;
-};
-__device__ constexpr NsPhase kNsPhases[3][10] = {
-    {{kNsGram, 0, 0, 0, kBufA, 0, 0, 0}, {kNsSquare, 0, kBufA, kBufA, kBufQ0, 0, 0, 0},
-     {kNsUpdate, 0, kBufQ0, 0, 0, 0, 0, 0}},
-    {{kNsGram, 0, 0, 0, kBufA, 0, 0, 0}, {kNsSquare, 0, kBufA, kBufA, kBufQ0, 0, 0, 0},
-     {kNsMul, 0, kBufQ0, kBufA, kBufT, 0, 0, 0}, {kNsMul, 0, kBufT, kBufQ0, kBufA, 0, 0, 0},
-     {kNsSquare, 0, kBufA, kBufA, kBufP, 0, 0, 0}, {kNsMul, 0, kBufP, kBufQ0, kBufQ1, 0, 0, 0},
-     {kNsUpdate, 0, kBufQ1, 0, 0, 0, 0, 0}},
-    {{kNsGram, 0, 0, 0, kBufA, 0, 0, 0}, {kNsSquare, 0, kBufA, kBufA, kBufQ0, 0, 0, 0},
-     {kNsMul, 0, kBufQ0, kBufA, kBufT, 0, 0, 0}, {kNsMul, 0, kBufT, kBufQ0, kBufA, 0, 0, 0},
-     {kNsSquare, 0, kBufA, kBufA, kBufP, 0, 0, 0}, {kNsMul, 1, kBufP, kBufA, kBufT, kBufP, kBufQ0, kBufQ1},
-     {kNsMul, 0, kBufT, kBufP, kBufA, 0, 0, 0}, {kNsSquare, 0, kBufA, kBufA, kBufP, 0, 0, 0},
-     {kNsMul, 0, kBufP, kBufQ1, kBufQ0, 0, 0, 0}, {kNsUpdate, 0, kBufQ0, 0, 0, 0, 0, 0}},
-};
-__device__ constexpr int kNsPhaseCount[3] = {3, 7, 10};
-
-// Walks the phases; every role of every CTA takes the same ones.
+// Walks the phases; every role of every CTA takes the same ones.  A matrix's
+// phase begins when its last one is complete.
 struct NsSeq {
-  int ph = -1;     // phases begun, less one
-  int group = 0;   // X of this group is in buffer group & 1
-  int left, size;  // steps left, this group's included; its steps
-  int pos = -1;
+  int kind = -1;
+  int step = 0;       // X of this step is in buffer step & 1
   unsigned done = 0;  // arrivals of a matrix's units in the phases before this one
-  NsPhase f;
-  __device__ __forceinline__ explicit NsSeq(const NsParams& p) : left(p.steps), size(min(p.first, p.steps)) {}
   __device__ __forceinline__ bool next(const NsParams& p) {
-    if (++ph > 0) done += static_cast<unsigned>(p.geo[geo()].arrivals);
-    if (++pos == kNsPhaseCount[size - 1]) {
-      left -= size;
-      if (left == 0) return false;
-      ++group;
-      size = min(p.later, left);
-      pos = 0;
+    if (kind >= 0) done += static_cast<unsigned>(p.geo[kind].arrivals);
+    if (++kind == kNsKinds) {
+      kind = 0;
+      ++step;
     }
-    f = kNsPhases[size - 1][pos];
-    return true;
+    return step < p.steps;
   }
-  __device__ __forceinline__ bool last_group() const { return left == size; }
-  __device__ __forceinline__ int geo() const {
-    return f.kind == kNsGram ? kGeoGram : (f.kind == kNsUpdate ? kGeoUpdate : (f.two ? kGeoSym2 : kGeoSym));
-  }
+  __device__ __forceinline__ bool first() const { return step == 0 && kind == 0; }
 };
 
 // 3-D tiled copies (x, y, batch).  PAIR: the barrier may be the other CTA's.
@@ -301,9 +265,9 @@ __device__ __forceinline__ int add_acq_rel_cta(int* addr, int v) {
   return old;
 }
 
-// A unit of work: a tile (product, matrix, row tile, column tile) and its k-blocks.
+// A unit of work: a tile (matrix, row tile, column tile) and its k-blocks.
 struct NsUnit {
-  int job, bz, rt, ct;
+  int bz, rt, ct;
   int kb0, kb1;
   int part;   // which of a split tile's parts (-1: a whole tile)
   int split;  // the split tile's number
@@ -314,7 +278,7 @@ struct NsUnit {
 // row (row i starts at block i (i + 1) / 2), each of kM / kN tiles.  Otherwise the tiles that share the longer
 // side's operand follow each other.
 template <bool SYM, class T>
-__device__ __forceinline__ NsUnit ns_unit_of(const NsGeo& g, int batch, int u) {
+__device__ __forceinline__ NsUnit ns_unit_of(const NsGeo& g, int u) {
   NsUnit n;
   int t = u;
   n.part = -1;
@@ -335,8 +299,6 @@ __device__ __forceinline__ NsUnit ns_unit_of(const NsGeo& g, int batch, int u) {
   }
   n.bz = t / g.tiles;
   t -= n.bz * g.tiles;
-  n.job = n.bz >= batch ? 1 : 0;
-  n.bz -= n.job * batch;
   if (SYM) {
     constexpr int kParts = T::kM / T::kN;
     const int part = t % kParts;
@@ -358,12 +320,12 @@ __device__ __forceinline__ NsUnit ns_unit_of(const NsGeo& g, int batch, int u) {
 
 template <class T>
 __device__ __forceinline__ NsUnit ns_unit(const NsParams& p, const NsSeq& s, int u) {
-  const int g = s.geo();
-  return g == kGeoUpdate ? ns_unit_of<false, T>(p.geo[g], p.batch, u) : ns_unit_of<true, T>(p.geo[g], p.batch, u);
+  const NsGeo& g = p.geo[s.kind];
+  return s.kind == kNsUpdate ? ns_unit_of<false, T>(g, u) : ns_unit_of<true, T>(g, u);
 }
 
 __device__ __forceinline__ int ns_units(const NsParams& p, const NsSeq& s) {
-  const NsGeo& g = p.geo[s.geo()];
+  const NsGeo& g = p.geo[s.kind];
   return g.whole + g.rest * g.splits;
 }
 
@@ -371,7 +333,7 @@ __device__ __forceinline__ int ns_units(const NsParams& p, const NsSeq& s) {
 // the first) did not: a matrix, all of them (p.batch), or nothing (-1).
 __device__ __forceinline__ int ns_need(const NsParams& p, const NsSeq& s, const NsUnit& n, int& waited) {
   const int need = p.few && n.part < 0 ? n.bz : p.batch;
-  if (s.ph == 0 || need == waited || waited == p.batch) return -1;
+  if (s.first() || need == waited || waited == p.batch) return -1;
   waited = need;
   return need;
 }
@@ -389,18 +351,16 @@ struct NsOperand {
   }
 };
 
-__device__ __forceinline__ void ns_operands(const NsParams& p, const NsSeq& s, int job, NsOperand& P, NsOperand& Q) {
-  const int l = job ? s.f.l2 : s.f.l, r = job ? s.f.r2 : s.f.r;
-  const NsMaps* x = &p.X[s.group & 1];
-  if (s.f.kind == kNsGram) {
+__device__ __forceinline__ void ns_operands(const NsParams& p, const NsSeq& s, NsOperand& P, NsOperand& Q) {
+  const NsMaps* x = &p.X[s.step & 1];
+  if (s.kind == kNsGram) {
     P = Q = NsOperand{x, p.tall ? kNsMN : kNsK};
-  } else if (s.f.kind == kNsUpdate) {
-    const NsOperand sl{&p.S[l], kNsSym};
-    P = p.tall ? NsOperand{x, kNsK} : sl;
-    Q = p.tall ? sl : NsOperand{x, kNsMN};
+  } else if (s.kind == kNsSquare) {
+    P = Q = NsOperand{&p.S[kBufA], kNsSym};
   } else {
-    P = NsOperand{&p.S[l], kNsSym};
-    Q = NsOperand{&p.S[r], kNsSym};
+    const NsOperand sp{&p.S[kBufP], kNsSym};
+    P = p.tall ? NsOperand{x, kNsK} : sp;
+    Q = p.tall ? sp : NsOperand{x, kNsMN};
   }
 }
 
@@ -453,19 +413,17 @@ __device__ __forceinline__ void ns_add4(uint32_t (&v)[32], int j, const float4& 
 // and bound the update at 20 us a tile.)  Sixteen warps with a quarter of the
 // columns each, or tensor-memory loads of 8 columns in a small loop, were
 // slower.  Returns false if a wait gave up.
-// KIND kNsGram: gram or product (a product has a correction on the diagonal).
 template <int KIND, class T>
-__device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, const NsUnit& n, int gen, int acc,
-                                            uint32_t parity, uint64_t* tfull, NsEpi& e, const WaitCtx& w) {
+__device__ __forceinline__ bool ns_epilogue(const NsParams& p, int step, const NsUnit& n, int acc, uint32_t parity,
+                                            uint64_t* tfull, NsEpi& e, const WaitCtx& w) {
   constexpr int kHalf = T::kHalf;
   constexpr int kBlks = T::kBlks;
-  const int gi = s.geo();
-  const NsGeo& g = p.geo[gi];
-  const int buf_l = n.job ? s.f.l2 : s.f.l, buf_r = n.job ? s.f.r2 : s.f.r, buf_out = n.job ? s.f.out2 : s.f.out;
-  const int par = s.group & 1;
-  const bool last = s.last_group();
-  const bool in_low = KIND == kNsUpdate && (!last || s.group == 0);  // X has a low part
-  const bool has_low = KIND == kNsUpdate && s.left > s.size && s.left - s.size > min(p.later, s.left - s.size);
+  const NsGeo& g = p.geo[KIND];
+  constexpr int kOut = KIND == kNsGram ? kBufA : kBufP;  // (of a symmetric result)
+  const int par = step & 1;
+  const bool last = step == p.steps - 1;
+  const bool in_low = KIND == kNsUpdate && (!last || step == 0);  // X has a low part
+  const bool has_low = KIND == kNsUpdate && step < p.steps - 2;   // the next step reads one
   const CUtensorMap* in0 = KIND == kNsSquare ? &p.Sbox[kBufA] : &p.Hbox[par];
   const CUtensorMap* in1 = &p.Lbox[par];
   const int lane = e.lane;
@@ -476,7 +434,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
   // The diagonal of P: of the row of P X, of the column of X P.  Written by
   // other CTAs of this launch: read through L2.
   const bool by_col = KIND == kNsUpdate && p.tall;
-  const float2* dv = p.diag[buf_l] + static_cast<size_t>(n.bz) * (by_col ? g.cols : g.rows);
+  const float2* dv = p.diag[kBufP] + static_cast<size_t>(n.bz) * (by_col ? g.cols : g.rows);
   float2 di = make_float2(0.f, 0.f);  // (d, f + d) of the row
   if (KIND == kNsUpdate && !by_col && live) {
     di = __ldcg(dv + row);
@@ -539,18 +497,17 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
     __syncwarp();
     int ok = 1;
     if (lane == 0) {
-      int* c = p.counters + p.batch + gi * kNsSplitCounters + n.split * T::kWarps + region;
+      int* c = p.counters + p.batch + KIND * kNsSplitCounters + n.split * T::kWarps + region;
       red_release_add(c, 1);
-      if (b0 < b1) ok = ns_count_wait(c, g.splits * (gen + 1), w) ? 1 : 0;
+      if (b0 < b1) ok = ns_count_wait(c, g.splits * (step + 1), w) ? 1 : 0;
     }
     __syncwarp();
     if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
   }
   // the result's scale, and the accumulator's share of it
-  const float so = buf_out == kBufA || buf_out == kBufT ? kNsScaleA : kNsScaleP;
+  constexpr float so = KIND == kNsGram ? kNsScaleA : kNsScaleP;
   const float sc = KIND == kNsSquare ? p.c * (kNsScaleP / (kNsScaleA * kNsScaleA))
-                                     : (KIND == kNsGram && s.f.kind == kNsGram ? kNsScaleA / (kNsScaleX * kNsScaleX)
-                                                                              : 1.f / kNsScaleP);
+                                     : (KIND == kNsGram ? kNsScaleA / (kNsScaleX * kNsScaleX) : 1.f / kNsScaleP);
 #pragma unroll 1
   for (int b = b0; b < b1; ++b, ++e.cnt) {
     const int c32 = col0 + b * 32;
@@ -638,10 +595,10 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
       // the block of this row's diagonal entry, column `lane`
       float corr = 0.f, dval = 0.f;
       const size_t at = static_cast<size_t>(n.bz) * g.rows + (live ? row : 0);
-      if (s.f.kind != kNsGram) {
-        const float2 l = __ldcg(p.diag[buf_l] + at), q = __ldcg(p.diag[buf_r] + at);
-        corr = fmaf(l.x, q.y, fmaf(l.y, q.x, l.x * q.x)) * so;
-        if (KIND == kNsSquare) corr = fmaf(p.c, corr, fmaf(p.b, l.x, p.a) * so);
+      if (KIND == kNsSquare) {
+        const float2 q = __ldcg(p.diag[kBufA] + at);
+        corr = fmaf(q.x, q.y, fmaf(q.y, q.x, q.x * q.x)) * so;
+        corr = fmaf(p.c, corr, fmaf(p.b, q.x, p.a) * so);
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -652,7 +609,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
         r[i] = f2_set(x.x, x.y);
       }
       const float f = __half2float(__float2half_rn(dval));
-      if (live) p.diag[buf_out][at] = make_float2((dval - f) / so, f / so);
+      if (live) p.diag[kOut][at] = make_float2((dval - f) / so, f / so);
     }
     uint32_t o[16];
     if (KIND == kNsUpdate && last) {
@@ -684,7 +641,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, const NsSeq& s, c
     fence_async_smem();
     __syncwarp();
     if (lane == 0) {
-      const CUtensorMap* m = KIND != kNsUpdate ? &p.Sbox[buf_out] : (last ? &p.Obox : &p.Hbox[par ^ 1]);
+      const CUtensorMap* m = KIND != kNsUpdate ? &p.Sbox[kOut] : (last ? &p.Obox : &p.Hbox[par ^ 1]);
       tma_store_3d(m, S0, c32, row0, n.bz);
       if (has_low) tma_store_3d(&p.Lbox[par ^ 1], S1, c32, row0, n.bz);
       bulk_commit();
@@ -782,13 +739,13 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     bool ok = true;
     const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
     const uint32_t smem0 = smem_u32(smem) + (left ? 0 : T::kLeftBytes);
-    for (NsSeq s(p); ok && s.next(p);) {
+    for (NsSeq s; ok && s.next(p);) {
       const int nunits = ns_units(p, s);
       int waited = -1;
       for (int u = first; ok && u < nunits; u += step) {
         const NsUnit n = ns_unit<T>(p, s, u);
         NsOperand P, Q;
-        ns_operands(p, s, n.job, P, Q);
+        ns_operands(p, s, P, Q);
         NsOperand op = left ? P : Q;
         const int row = left ? n.rt * T::kM : n.ct * T::kN;
         int mn = op.template first_mn<T::kM>(row), r0 = row + rank * 128;
@@ -857,12 +814,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       bool ok = true;
       const uint32_t smem0 = smem_u32(smem);
       constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
-      for (NsSeq s(p); ok && s.next(p);) {
+      for (NsSeq s; ok && s.next(p);) {
         const int nunits = ns_units(p, s);
         for (int u = first; ok && u < nunits; u += step, ++it) {
           const NsUnit n = ns_unit<T>(p, s, u);
           NsOperand P, Q;
-          ns_operands(p, s, n.job, P, Q);
+          ns_operands(p, s, P, Q);
           const int acc = it & 1;
           if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, w))) {
             ok = false;
@@ -942,11 +899,8 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     int it = 0;
     bool ok = true;
     int waits = 0;
-    uint64_t gens = 0;  // phases of each geometry so far, 16 bits each
-    for (NsSeq s(p); ok && s.next(p);) {
+    for (NsSeq s; ok && s.next(p);) {
       const int nunits = ns_units(p, s);
-      const int gen = static_cast<int>(gens >> (16 * s.geo())) & 0xffff;
-      gens += 1ull << (16 * s.geo());
       int waited = -1, arrive = 0;
       for (int u = first; ok && u < nunits; u += step, ++it) {
         const NsUnit n = ns_unit<T>(p, s, u);
@@ -960,12 +914,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         }
         const int acc = it & 1;
         const uint32_t par = (it >> 1) & 1;
-        if (s.f.kind == kNsSquare)
-          ok = ns_epilogue<kNsSquare, T>(p, s, n, gen, acc, par, tfull, e, w);
-        else if (s.f.kind == kNsUpdate)
-          ok = ns_epilogue<kNsUpdate, T>(p, s, n, gen, acc, par, tfull, e, w);
+        if (s.kind == kNsSquare)
+          ok = ns_epilogue<kNsSquare, T>(p, s.step, n, acc, par, tfull, e, w);
+        else if (s.kind == kNsUpdate)
+          ok = ns_epilogue<kNsUpdate, T>(p, s.step, n, acc, par, tfull, e, w);
         else
-          ok = ns_epilogue<kNsGram, T>(p, s, n, gen, acc, par, tfull, e, w);
+          ok = ns_epilogue<kNsGram, T>(p, s.step, n, acc, par, tfull, e, w);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {

@@ -122,7 +122,7 @@ constexpr int kNsMaxNormBlocks = 1184;  // eight for each of 148 SMs
 // waits for its own matrix (ns_kernel has the figures).
 constexpr int kNsFew = 4;
 
-inline int ns_counters(int64_t batch) { return static_cast<int>(batch) + kGeos * kNsSplitCounters; }
+inline int ns_counters(int64_t batch) { return static_cast<int>(batch) + kNsKinds * kNsSplitCounters; }
 
 // (byte strides of the tensor maps; tiles are counted in ints)
 inline bool ns_shape_ok(int64_t batch, int64_t m, int64_t n) {
@@ -134,7 +134,6 @@ struct NsPlan {
   int64_t batch, m, n, s;  // s: the smaller side
   bool tall;
   int tile;                // 256: 256 x 256 tiles on CTA pairs; 128, 64: 128 x tile
-  bool grouped;            // steps in groups of up to three
   int norm_blocks;
   size_t hi[2], lo[2], sym[kBufs], diag[kBufs], sums, counters, part, bytes;
 };
@@ -147,25 +146,24 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
   p.tall = m > n;
   p.s = p.tall ? n : m;
   // CTA pairs (half of the operand traffic) where their 256 x 256 tiles fill more
-  // than one round of the 74 pairs: with a long K those of X (323 against 385 us
-  // for two of 2048 x 2048, 591 against 790 for four, 1050 against 1500 at 4096 x
-  // 4096), with a shorter one those of the square matrices too, whose phases are
-  // most of a step (313 against 389 for twelve of 1024 x 1024, 437 against 493 for
-  // sixteen), or several rounds of X's (425 against 458 at 1024 x 32768).  With
-  // fewer the four times as many small ones end sooner: 201 against 265 at 1024 x
-  // 4096, 312 against 377 for four of them; eight of 1024 x 1024 (240) and 2048 x
-  // 2048 (251) are equal.  The smallest where all of them run at once: 94 against
-  // 113 us at 512 x 512, 73 against 91 at 256 x 256.
+  // than one round of the 74 pairs, in us against the 128 x 128 tiles: with a
+  // long K those of X (319 against 381 for two of 2048 x 2048, 582 against 795 for
+  // four, 1030 against 1490 at 4096 x 4096), with a shorter one those of the square
+  // matrices too, whose phases are most of a step (310 against 409 for twelve of
+  // 1024 x 1024, 442 against 506 for sixteen), or, of a long side, several rounds
+  // of X's (691 against 854 at 1024 x 32768, 428 against 463 at 1024 x 16384, 469
+  // against 538 at 512 x 32768; for five of 1024 x 4096 500 against 541, but for
+  // four 418 against 393: a batch's square phases have more tiles).  With fewer
+  // the four times as many small ones end sooner: 193 against 203 at 1024 x 4096,
+  // 303 against 325 at 1152 x 8192; eight of 1024 x 1024 (255) are equal.  The
+  // smallest where all of them run at once: 94 against 113 us at 512 x 512, 73
+  // against 91 at 256 x 256.
   const int64_t t256 = batch * ((m + 255) / 256) * ((n + 255) / 256);
   const int64_t s256 = (p.s + 255) / 256, square = batch * s256 * s256;
-  const bool pairs = p.s >= 1536 ? t256 >= 100 : p.s >= 1024 && (square >= 150 || t256 >= 400);
+  const bool pairs = p.s >= 1536 ? t256 >= 100
+                                 : (p.s >= 1024 && square >= 150) ||
+                                       (p.s >= 512 && std::max(m, n) >= 2 * p.s && t256 >= (batch == 1 ? 180 : 300));
   p.tile = pairs ? 256 : batch * ((m + 127) / 128) * ((n + 63) / 64) <= 148 ? 64 : 128;
-  // Groups save 9 s^2 l operations of five steps and cost 9 s^3 and two more
-  // phases: 626 against 984 us at 2048 x 16384, 298 against 367 at 2048 x 4096,
-  // 164 against 173 at 1024 x 2560, but 152 against 148 at 1024 x 2048 and 253
-  // against 251 at 2048 x 2048.  Below 512 they would save little and cost
-  // accuracy (2.6e-3 against 2.0e-3 of |X|_F, the output's rounding included).
-  p.grouped = p.s >= 512 && (p.tall ? m : n) >= 2 * p.s;
   const int64_t n8 = m * n / 8;
   p.norm_blocks = static_cast<int>(std::min<int64_t>(kNsMaxNormBlocks, (n8 + 2047) / 2048));
   size_t o = 0;
@@ -179,9 +177,8 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n) {
     p.lo[i] = take(static_cast<size_t>(batch) * m * n * 2);
   }
   for (int i = 0; i < kBufs; ++i) {
-    const bool used = p.grouped || i == kBufA || i == kBufQ0;
-    p.sym[i] = take(used ? static_cast<size_t>(batch) * p.s * p.s * 2 : 0);
-    p.diag[i] = take(used ? static_cast<size_t>(batch) * p.s * 8 : 0);
+    p.sym[i] = take(static_cast<size_t>(batch) * p.s * p.s * 2);
+    p.diag[i] = take(static_cast<size_t>(batch) * p.s * 8);
   }
   p.sums = take(static_cast<size_t>(batch) * p.norm_blocks * 8);
   p.counters = take(static_cast<size_t>(ns_counters(batch)) * 4);
@@ -273,15 +270,13 @@ coda_status_t ns_launch(int dev, DevInfo* info, NsParams& p, const NsPlan& pl, c
     }
   }
   const int64_t s = pl.s, l = pl.tall ? pl.m : pl.n;
-  p.geo[kGeoGram] = ns_geo(pl.batch, s, s, l, true, N, slots[dev]);
-  p.geo[kGeoSym] = ns_geo(pl.batch, s, s, s, true, N, slots[dev]);
-  p.geo[kGeoSym2] = ns_geo(2 * pl.batch, s, s, s, true, N, slots[dev]);
-  p.geo[kGeoSym2].arrivals *= 2;  // two products of a matrix
-  p.geo[kGeoUpdate] = ns_geo(pl.batch, pl.m, pl.n, s, false, N, slots[dev]);
+  p.geo[kNsGram] = ns_geo(pl.batch, s, s, l, true, N, slots[dev]);
+  p.geo[kNsSquare] = ns_geo(pl.batch, s, s, s, true, N, slots[dev]);
+  p.geo[kNsUpdate] = ns_geo(pl.batch, pl.m, pl.n, s, false, N, slots[dev]);
   int n = 0, units = 0;
   for (const NsGeo& g : p.geo) {
     n = std::max(n, g.whole > 0 ? slots[dev] : g.rest * g.splits);
-    if (pl.grouped || &g != &p.geo[kGeoSym2]) units = std::max(units, g.whole + g.rest * g.splits);
+    units = std::max(units, g.whole + g.rest * g.splits);
   }
   p.few = pl.batch > 1 && units <= kNsFew * slots[dev];
   p.wait_ns = static_cast<uint64_t>(g_wait_ns);
@@ -508,8 +503,6 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
   p.batch = static_cast<int>(batch);
   p.steps = steps;
   p.tall = pl.tall ? 1 : 0;
-  p.first = pl.grouped ? 3 : 1;
-  p.later = pl.grouped ? 2 : 1;
   p.a = a;
   p.b = b;
   p.c = c;
@@ -519,7 +512,6 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
     ok = ok && ns_maps(&p.X[i], hi[i], n, m, batch) && tmap3d(&p.Hbox[i], hi[i], false, n, m, batch, 32, 32) &&
          tmap3d(&p.Lbox[i], lo[i], false, n, m, batch, 32, 32);
   for (int i = 0; i < kBufs; ++i) {
-    if (!pl.grouped && i != kBufA && i != kBufQ0) continue;
     const void* b = w + pl.sym[i];
     ok = ok && ns_maps(&p.S[i], b, s, s, batch) && tmap3d(&p.Sbox[i], b, false, s, s, batch, 32, 32);
   }

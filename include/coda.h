@@ -554,7 +554,7 @@ coda_status_t coda_add_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const 
                                    size_t ws_bytes, int64_t M, int64_t N, void* stream);
 
 /* Bytes of workspace coda_newton_schulz needs (0 for a bad shape): X twice in
- * two fp16 parts, and two to five square fp16 matrices of the smaller side. */
+ * two fp16 parts, and two square fp16 matrices of the smaller side. */
 size_t coda_newton_schulz_workspace_size(int64_t batch, int64_t m, int64_t n);
 
 /* Newton-Schulz orthogonalisation of `batch` matrices (the step of the Muon
@@ -562,14 +562,14 @@ size_t coda_newton_schulz_workspace_size(int64_t batch, int64_t m, int64_t n);
  *   A = X X^T;  X <- a X + (b A + c A^2) X      (X^T X and the other side if m > n)
  * and out = bf16(X).  G [batch, m, n] fp32 (a gradient or momentum, such as the
  * backward calls give), out [batch, m, n] bf16.  The products take fp16
- * operands with fp32 sums and corrections for their rounding: about 1e-3 of
- * |X|_F from exact arithmetic before the output's rounding; up to 1e-2 for a
- * nearly low-rank G whose larger side is at least twice the smaller one (of 512
- * or more), where several steps are taken on the smaller side.  The coefficients
- * must keep the singular values bounded, as Muon's (3.4445, -4.775, 2.0315)
- * do: intermediate values beyond 16 (X) or 64 (A, b A + c A^2) become
- * infinite.  A matrix with a non-finite entry gives a non-finite result and
- * leaves the others of the batch alone; a zero matrix gives zeros if eps > 0.
+ * operands with fp32 sums and corrections for their rounding: after five steps
+ * about 1e-3 of |X|_F from exact arithmetic before the output's rounding (itself
+ * 1.7e-3), and where one or a few directions hold G's norm up to 1.5e-3 + 0.65 /
+ * min(m, n).  The coefficients must keep the singular values bounded, as Muon's
+ * (3.4445, -4.775, 2.0315) do: intermediate values beyond 16 (X), 64 (A) or
+ * 256 (a I + b A + c A^2) become infinite.  A matrix with a non-finite entry
+ * gives a non-finite result and leaves the others of the batch alone; a zero
+ * matrix gives zeros if eps > 0.
  * m and n multiples of 8, m * n <= 2^38, 1 <= steps <= 100, batch <= 65535. */
 coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, int64_t m, int64_t n, int steps, float a,
                                  float b, float c, float eps, void* ws, size_t ws_bytes, void* stream);
