@@ -72,6 +72,7 @@ constexpr int kNsRightWarp = 2 + kNsEpiWarps;
 // stages of one k-block each, and two accumulators).
 constexpr int kNsAhead = 16;
 constexpr int kNsBoxBytes = 32 * 32 * 2;  // a 32 x 32 box of an epilogue
+constexpr uint64_t kNsDrainNs = 10000000;  // 10 ms: copies land within microseconds
 
 // A tile's shape and what a CTA keeps for it in shared memory.  N = 256: a
 // cluster of two CTAs per 256 x 256 tile (cta_group::2; rank r owns accumulator
@@ -395,6 +396,7 @@ struct NsEpi {
   int lane;
   uint32_t cnt;       // blocks done: block i uses buffer i & 1
   uint32_t loads;     // bit i: parity of buffer i's next load
+  uint32_t flying;    // bit i: buffer i's load has not been waited for
 };
 
 // v[4 j ..] += o
@@ -453,12 +455,13 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, int step, const N
   auto fetch = [&](int b, uint32_t cnt) {
     if (KIND == kNsGram) return;
     const int c = col0 + b * 32;
+    e.flying |= 1u << (cnt & (T::kBufs - 1));
     if (lane == 0) {
       bulk_wait_read<0>();  // the buffer's last store has left it
       uint8_t* d = e.stg + (cnt & (T::kBufs - 1)) * (2 * kNsBoxBytes);
       mbar_arrive_expect_tx(&e.bars[cnt & (T::kBufs - 1)], in_low ? 2 * kNsBoxBytes : kNsBoxBytes);
       tma_load_3d<false>(smem_u32(d), in0, smem_u32(&e.bars[cnt & (T::kBufs - 1)]), c, row0, n.bz);
-      if (in_low) 
+      if (in_low)
         tma_load_3d<false>(smem_u32(d + kNsBoxBytes), in1, smem_u32(&e.bars[cnt & (T::kBufs - 1)]), c, row0, n.bz);
     }
     if (by_col && c + lane < g.cols) {
@@ -522,6 +525,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, int step, const N
       if (b + 1 < b1) fetch(b + 1, e.cnt + 1);
       if (!__all_sync(0xffffffffu, mbar_wait(&e.bars[buf], (e.loads >> buf) & 1, w))) return false;
       e.loads ^= 1u << buf;
+      e.flying &= ~(1u << buf);
     }
     uint4 x0[4], x1[4];
 #pragma unroll
@@ -724,6 +728,9 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const WaitCtx w{abort_flag, p.wait_ns};
+  // Copies and MMAs in flight are waited for at the end, after a wait that gave up
+  // too, however short the caller's limit is.
+  const uint64_t drain_ns = p.wait_ns > kNsDrainNs ? p.wait_ns : kNsDrainNs;
 
   // The issuing warps run as whole warps, with one elected thread issuing: the
   // instructions take their operands from uniform registers, and in code of a
@@ -802,7 +809,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         --stage;
       }
       int no_abort = 0;
-      (void)mbar_wait(PAIR ? &empty[stage] : &full[stage], phase, WaitCtx{&no_abort, p.wait_ns});
+      (void)mbar_wait(PAIR ? &empty[stage] : &full[stage], phase, WaitCtx{&no_abort, drain_ns});
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -881,7 +888,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           tc_commit(drain);
       }
       int no_abort = 0;
-      (void)mbar_wait(drain, 0, WaitCtx{&no_abort, p.wait_ns});
+      (void)mbar_wait(drain, 0, WaitCtx{&no_abort, drain_ns});
       __syncwarp();
     }
   } else {
@@ -894,6 +901,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     e.bars = ebars + 2 * (warp - 2);
     e.cnt = 0;
     e.loads = 0;
+    e.flying = 0;
     e.taddr = tmem_base + (static_cast<uint32_t>(e.q * 32) << 16);
     const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
     int it = 0;
@@ -946,6 +954,11 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         }
         arrive = 0;
       }
+    }
+    // (a wait that gave up leaves loads behind)
+    for (int i = 0; i < T::kBufs; ++i) {
+      int no_abort = 0;
+      if ((e.flying >> i) & 1) (void)mbar_wait(&e.bars[i], (e.loads >> i) & 1, WaitCtx{&no_abort, drain_ns});
     }
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
