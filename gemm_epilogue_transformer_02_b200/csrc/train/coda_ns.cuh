@@ -764,7 +764,11 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             const int b0 = need < p.batch ? need : 0, b1 = need < p.batch ? need + 1 : (p.few ? p.batch : 1);
             const unsigned target = p.few ? s.done : s.done * static_cast<unsigned>(p.batch);
             for (int b = b0 + lane; b < b1; b += 32) passed = passed && ns_count_wait(p.counters + b, target, w);
-            if (b1 - b0 > 1) passed = __all_sync(0xffffffffu, passed);
+            if (b1 - b0 > 1) {
+              // each lane has acquired its counters: the arrival of lane 0 hands on all of them
+              __syncwarp();
+              passed = __all_sync(0xffffffffu, passed);
+            }
             if (lane == 0 && passed) mbar_arrive(&go[it & (kNsAhead - 1)]);
           } else {
             passed = mbar_wait(&go[it & (kNsAhead - 1)], (it / kNsAhead) & 1, w);
