@@ -3,8 +3,8 @@
 //   h = x + res;  r = 1 / sqrt(mean(h^2) + eps);  y = gamma * h * r
 //   forward   h in bf16 and y as e4m3, with the scales the 8-bit GEMMs take
 //             (one power of two per 32 columns, or one per tensor)
-//   backward  g = dy * gamma;  dx = r g - r^3 mean(g h) h + d_h;
-//             dgamma = sum_i dy h r
+//   backward  g = dy * gamma;  dx = r g - r (r mean(g h)) (r h) + d_h;
+//             dgamma = sum_i dy (r h)
 //
 // Each element is read once and each output written once; both are bound by
 // HBM (7 and 8 bytes an element).  A row lives in the registers of one block
@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_bwd_kernel(
     }
     const float ri = __ldg(r + row);
     if (kAhead) load(row + step);
-    const float coef = -ri * ri * ri * norm8_sum<WARP>(s, red[it]) / static_cast<float>(N);
+    // (r^3 would leave fp32 for rows 1e13 away from one: r meets the sum and h first)
+    const float coef = -ri * norm8_sum<WARP>(s, red[it]) / static_cast<float>(N) * ri;
     const size_t ro = static_cast<size_t>(row) * N;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
@@ -226,12 +227,12 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_bwd_kernel(
       uint32_t o[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float ya = bf16lo(yw[e]) * ri, yb = bf16hi(yw[e]) * ri;
-        const float ha = bf16lo(hw[e]), hb = bf16hi(hw[e]);
+        const float ya = bf16lo(yw[e]), yb = bf16hi(yw[e]);
+        const float ha = bf16lo(hw[e]) * ri, hb = bf16hi(hw[e]) * ri;
         dg[k][2 * e] = fmaf(ya, ha, dg[k][2 * e]);
         dg[k][2 * e + 1] = fmaf(yb, hb, dg[k][2 * e + 1]);
-        o[e] = pack_bf16x2(fmaf(ya, bf16lo(gw[e]), fmaf(coef, ha, bf16lo(sw[e]))),
-                           fmaf(yb, bf16hi(gw[e]), fmaf(coef, hb, bf16hi(sw[e]))));
+        o[e] = pack_bf16x2(fmaf(ya * ri, bf16lo(gw[e]), fmaf(coef, ha, bf16lo(sw[e]))),
+                           fmaf(yb * ri, bf16hi(gw[e]), fmaf(coef, hb, bf16hi(sw[e]))));
       }
       if (c < N) *reinterpret_cast<uint4*>(dx + ro + c) = make_uint4(o[0], o[1], o[2], o[3]);
     }

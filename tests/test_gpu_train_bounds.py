@@ -88,3 +88,37 @@ def test_newton_schulz_of_a_gradient_with_feature_means(m, n, means):
     G = (randn(g, m, T) + means * randn(g, m, 1)) @ (randn(g, T, n) + means * randn(g, 1, n))
     e, slack = ns_error(C.newton_schulz(G), ns_exact(G))
     assert e <= math.sqrt(stated(m, n) ** 2 + slack), e
+
+
+# --------------------------------------------------------------- 8-bit norm
+
+
+@pytest.mark.parametrize("M,N", [(5, 264), (40, 2048), (3, 8200)])
+@pytest.mark.parametrize("k", [-60, -45, 40, 60])
+def test_norm_backward_of_rows_far_from_one(M, N, k):
+    """dx of 2^k h with 2^-k r is 2^-k dx, and dgamma is the same, to the last bit:
+    every product only changes its exponent."""
+    g = gen(M + N)
+    h = randn(g, M, N).to(BF)
+    r = torch.rsqrt(h.float().square().mean(1))
+    dy, gamma = randn(g, M, N).to(BF), randn(g, N).to(BF)
+    dx, dgamma = C.add_rmsnorm_bwd(dy, h, r, gamma)
+    dx2, dgamma2 = C.add_rmsnorm_bwd(dy, h * 2.0 ** k, r * 2.0 ** -k, gamma)
+    assert torch.equal(dx2.float(), dx.float() * 2.0 ** -k) and torch.equal(dgamma2, dgamma)
+
+
+def test_norm_of_a_stream_far_from_one():
+    """The same forward and back: with eps 0 only the exponents of h and r change."""
+    M, N = 9, 640
+    g = gen(12)
+    x, gamma = randn(g, M, N).to(BF), randn(g, N).to(BF)
+    dy, d_h = randn(g, M, N).to(BF), randn(g, M, N).to(BF)
+    h, q, sf, r = C.add_rmsnorm_mx(x, x, gamma, 0.0)
+    dx, dgamma = C.add_rmsnorm_bwd(dy, h, r, gamma, d_h)
+    for k in (-58, 58):
+        s = 2.0 ** k
+        h2, q2, sf2, r2 = C.add_rmsnorm_mx(x * s, x * s, gamma, 0.0)
+        assert torch.equal(h2.float(), h.float() * s) and torch.equal(q2, q) and torch.equal(sf2, sf)
+        assert torch.equal(r2, r / s)
+        dx2, dgamma2 = C.add_rmsnorm_bwd(dy, h2, r2, gamma, (d_h / s).to(BF))
+        assert torch.equal(dx2.float(), dx.float() / s) and torch.equal(dgamma2, dgamma)
