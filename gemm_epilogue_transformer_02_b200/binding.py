@@ -928,8 +928,8 @@ def add_rmsnorm_mx(x, res, gamma, eps: float, *, h=True, h_out=None, yq_out=None
 
 def add_rmsnorm_fp8(x, res, gamma, eps: float, s_y, *, h=True, h_out=None, y8_out=None, amax_out=None, r_out=None):
     """h = x + res (res may be None), y8 = e4m3(gamma * h * r / s_y) for
-    gemm_fp8, amax = max |y|.  Returns (h bf16 or None, y8 uint8 [M, N], amax
-    [1], r [M])."""
+    gemm_fp8, amax = max |y| (no rows: 0, or amax_out as it was).  Returns (h
+    bf16 or None, y8 uint8 [M, N], amax [1], r [M])."""
     M, N = _matrix(x, BF16, "x")
     if res is not None:
         _ok(res, BF16, "res", (M, N))
@@ -937,6 +937,8 @@ def add_rmsnorm_fp8(x, res, gamma, eps: float, s_y, *, h=True, h_out=None, y8_ou
     _ok(s_y, F32, "s_y", (1,))
     h_out = _out_like(h_out, "h_out", x) if h else None
     y8_out = _out_like(y8_out, "y8_out", x, U8)
+    if M == 0 and amax_out is None:
+        amax_out = torch.zeros_like(s_y)  # (the library writes none)
     amax_out = _out_like(amax_out, "amax_out", s_y)
     r_out = _out(r_out, F32, "r_out", (M,), x)
     _launch("coda_add_rmsnorm_fp8", (x, res, gamma, s_y, h_out, y8_out, amax_out, r_out), x.data_ptr(), _addr(res),

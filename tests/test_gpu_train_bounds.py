@@ -122,3 +122,13 @@ def test_norm_of_a_stream_far_from_one():
         assert torch.equal(r2, r / s)
         dx2, dgamma2 = C.add_rmsnorm_bwd(dy, h2, r2, gamma, (d_h / s).to(BF))
         assert torch.equal(dx2.float(), dx.float() / s) and torch.equal(dgamma2, dgamma)
+
+
+def test_amax_of_an_empty_batch_is_zero():
+    """A new amax is never left as it was allocated (a given one stays as it is)."""
+    old = [torch.full((1,), 3.0, device="cuda") for _ in range(64)]
+    del old  # the allocator's next small blocks hold 3
+    for N in (16, 512, 2048):
+        e, gamma = torch.empty(0, N, dtype=BF, device="cuda"), torch.ones(N, dtype=BF, device="cuda")
+        amax = C.add_rmsnorm_fp8(e, None, gamma, 1e-6, torch.ones(1, device="cuda"))[2]
+        assert float(amax) == 0.0
