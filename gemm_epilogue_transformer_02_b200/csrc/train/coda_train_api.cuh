@@ -37,8 +37,9 @@ coda_status_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t 
 // ---------------------------------------------------------------- embedding
 
 // Pairs per block of the embedding backward: 16, so that a batch of some
-// thousand tokens gives some hundred blocks; more once that would make over
-// 2048 blocks, which bounds the parts a run over many chunks is joined from.
+// thousand tokens gives some hundred blocks; more once that would make over 2048
+// blocks, which bounds the parts a run over many chunks is joined from (up to
+// 2^21 rows: from there on a block takes 1024 pairs).
 inline int embed_chunk(int64_t M) {
   int64_t c = 16;
   while (c < coda::kEmbBwdMaxChunk && M > 2048 * c) c *= 2;
@@ -66,6 +67,24 @@ inline EmbedWs embed_ws(int64_t M, int64_t D, int64_t V) {
   w.bitmap = w.crossing + 256;
   w.bytes = w.bitmap + align256(w.words * 4);
   return w;
+}
+
+// Spans of columns of the summing blocks, and 2^unit rows of a zeroing one: about
+// 64 KB, so that the blocks that run together write a compact range.
+inline int embed_bwd_spans(int64_t D) {
+  return static_cast<int>((D + 8 * coda::kEmbBwdThreads - 1) / (8 * coda::kEmbBwdThreads));
+}
+inline int embed_bwd_unit(int64_t D) {
+  int unit = 0;
+  while (unit < 5 && ((D * 4) << (unit + 1)) <= 65536) ++unit;
+  return unit;
+}
+
+// (blocks are counted in ints)
+inline bool embed_bwd_shape_ok(int64_t M, int64_t D, int64_t V) {
+  return M >= 0 && M <= kEmbBwdMaxRows && dim_ok(D) && V > 0 && V < kMaxInt &&
+         (M + embed_chunk(M) - 1) / embed_chunk(M) * embed_bwd_spans(D) < kMaxInt / 2 &&
+         (V >> embed_bwd_unit(D)) < kMaxInt / 2;
 }
 
 // Bytes of dE that the sorting launch zeroes: as many as HBM takes while one
@@ -294,6 +313,10 @@ extern "C" {
 coda_status_t coda_embed(const int64_t* tokens, const uint16_t* E, float scale, const uint16_t* gamma, uint16_t* h_out,
                          uint16_t* hg_out, float* partial, int64_t M, int64_t D, int64_t V, void* stream) {
   CODA_CHECK(M >= 0 && M <= kMaxInt && dim_ok(D) && V > 0 && V < kMaxInt, CODA_ERR_SHAPE);
+  const int64_t nspan = (D + 255) / 256;
+  const int64_t items = (M + kEmbRows - 1) / kEmbRows * nspan;
+  const int64_t blocks = (items + kEmbWarps - 1) / kEmbWarps;
+  CODA_CHECK(blocks <= kMaxInt, CODA_ERR_SHAPE);
   if (M == 0) return CODA_OK;  // (an empty tensor has no address)
   CODA_CHECK(tokens && E && (h_out || hg_out || partial) && (!hg_out || gamma), CODA_ERR_NULL);
   CODA_CHECK(al16(tokens) && al16(E) && al16(gamma) && al16(h_out) && al16(hg_out) && al16(partial), CODA_ERR_ALIGN);
@@ -301,10 +324,6 @@ coda_status_t coda_embed(const int64_t* tokens, const uint16_t* E, float scale, 
   DevInfo* info;
   const coda_status_t st = current_device(&dev, &info);
   if (st != CODA_OK) return st;
-  const int64_t nspan = (D + 255) / 256;
-  const int64_t items = (M + kEmbRows - 1) / kEmbRows * nspan;
-  const int64_t blocks = (items + kEmbWarps - 1) / kEmbWarps;
-  CODA_CHECK(blocks <= kMaxInt, CODA_ERR_SHAPE);
   return launch_pdl(embed_kernel, dim3(static_cast<unsigned>(blocks)), 32 * kEmbWarps, 0, 0,
                     static_cast<cudaStream_t>(stream), tokens, reinterpret_cast<const __nv_bfloat16*>(E), scale,
                     reinterpret_cast<const __nv_bfloat16*>(gamma), reinterpret_cast<__nv_bfloat16*>(h_out),
@@ -313,13 +332,13 @@ coda_status_t coda_embed(const int64_t* tokens, const uint16_t* E, float scale, 
 }
 
 size_t coda_embed_bwd_workspace_size(int64_t M, int64_t D, int64_t V) {
-  if (M <= 0 || M > kEmbBwdMaxRows || !dim_ok(D) || V <= 0 || V >= kMaxInt) return 0;
+  if (M <= 0 || !embed_bwd_shape_ok(M, D, V)) return 0;
   return embed_ws(M, D, V).bytes;
 }
 
 coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float scale, float* dE, int accumulate, void* ws,
                              size_t ws_bytes, int64_t M, int64_t D, int64_t V, void* stream) {
-  CODA_CHECK(M >= 0 && M <= kEmbBwdMaxRows && dim_ok(D) && V > 0 && V < kMaxInt, CODA_ERR_SHAPE);
+  CODA_CHECK(embed_bwd_shape_ok(M, D, V), CODA_ERR_SHAPE);
   CODA_CHECK(dE && (M == 0 || (tokens && dh)), CODA_ERR_NULL);
   CODA_CHECK(al16(tokens) && al16(dh) && al16(dE) && al16(ws), CODA_ERR_ALIGN);
   CODA_CHECK(M == 0 || (ws && ws_bytes >= embed_ws(M, D, V).bytes), CODA_ERR_WORKSPACE);
@@ -383,14 +402,8 @@ coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float sc
                   bitmap, w.words, crossing);
   if (st != CODA_OK) return st;
   const int threads = static_cast<int>(std::min<int64_t>(kEmbBwdThreads, (D / 8 + 31) & ~int64_t(31)));
-  const int spans = static_cast<int>((D + 8 * kEmbBwdThreads - 1) / (8 * kEmbBwdThreads));
-  CODA_CHECK(static_cast<int64_t>(w.items) * spans < kMaxInt / 2, CODA_ERR_SHAPE);
-  // a zeroing block takes about 64 KB of rows, so that the blocks that run
-  // together write a compact range
-  int unit = 0;
-  while (unit < 5 && (row << (unit + 1)) <= 65536) ++unit;
+  const int spans = embed_bwd_spans(D), unit = embed_bwd_unit(D);
   const int64_t zb = accumulate ? 0 : (V - zero_row + (1 << unit) - 1) >> unit;
-  CODA_CHECK(zb < kMaxInt / 2, CODA_ERR_SHAPE);
   auto sum = accumulate ? embed_bwd_kernel<true> : embed_bwd_kernel<false>;
   st = launch_pdl(sum, dim3(static_cast<unsigned>(w.items * spans + zb)), threads, 0, 0, s, pairs,
                   reinterpret_cast<const __nv_bfloat16*>(dh), scale, dE, part, list, crossing, static_cast<int>(M), V,
