@@ -132,3 +132,34 @@ def test_amax_of_an_empty_batch_is_zero():
         e, gamma = torch.empty(0, N, dtype=BF, device="cuda"), torch.ones(N, dtype=BF, device="cuda")
         amax = C.add_rmsnorm_fp8(e, None, gamma, 1e-6, torch.ones(1, device="cuda"))[2]
         assert float(amax) == 0.0
+
+
+# ------------------------------------------------------- embedding gradient
+
+
+# Rows past the first 48 MiB + 4096 M bytes of dE are zeroed by blocks of 8, 8, 2
+# and 1 rows of a 32-row word of the bitmap.
+@pytest.mark.parametrize("D,V", [(2048, 8003), (1032, 16001), (4104, 4001), (16392, 1003)])
+@pytest.mark.parametrize("kind", ["none", "borders", "every third"])
+def test_embed_bwd_zeroes_every_row_that_does_not_occur(D, V, kind):
+    g = gen(D + V)
+    first = ((48 << 20) + 4096 * 64) // (32 * 4 * D) * 32
+    assert first < V - 64
+    if kind == "none":
+        tokens = torch.full((5,), -1, device="cuda")
+    elif kind == "borders":
+        at = [0, 31, 32, V - 1, V - 2]
+        for k in range(first - 64, first + 64, 8):
+            at += [k - 1, k, k + 1]
+        tokens = torch.tensor(sorted(set(at)), device="cuda")
+    else:
+        tokens = torch.arange(first - 40, V, 3, device="cuda")
+    tokens = tokens[torch.randperm(len(tokens), generator=g, device="cuda")]
+    dh = randn(g, len(tokens), D).to(BF)
+    raw = torch.full((V + 2, D), float("nan"), device="cuda")
+    dE = C.embed_bwd(tokens, dh, V, dE_out=raw[1:-1])
+    ref = torch.zeros(V, D, device="cuda")
+    if kind != "none":
+        ref[tokens] = dh.float()  # each occurs once
+    assert torch.equal(dE, ref)
+    assert bool(raw[0].isnan().all()) and bool(raw[-1].isnan().all())
