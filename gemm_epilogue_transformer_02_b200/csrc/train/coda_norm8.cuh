@@ -16,13 +16,13 @@
 
 namespace coda {
 
-// Sum over the row's threads, a warp or the block; every one gets it.  `red`
-// holds 32 floats; the caller synchronises before its next use.
+// Sum over the row's threads, a warp or the block (of two warps or more); every
+// one gets it.  `red` holds 32 floats; the caller synchronises before its next use.
 template <bool WARP>
 __device__ __forceinline__ float norm8_sum(float s, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (WARP || blockDim.x == 32) return s;
+  if (WARP) return s;
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
   s = red[threadIdx.x & 31];  // entries past the block's warps are zero
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_kernel(
     const int c = (tid + k * nt) * 8;
     gv[k] = c < cols ? __ldg(reinterpret_cast<const uint4*>(gamma + c)) : make_uint4(0, 0, 0, 0);
   }
-  if (!WARP && nt > 32) __syncthreads();  // `red` is cleared
+  if (!WARP) __syncthreads();  // `red` is cleared
   float h[VPT][8];
   float ss = 0.f;
 #pragma unroll
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_bwd_kernel(
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[k][e] = 0.f;
-  if (!WARP && nt > 32) __syncthreads();
+  if (!WARP) __syncthreads();
   int it = 0;
   for (int64_t row = first; row < M; row += step, it ^= 1) {
     if (!kAhead) load(row);

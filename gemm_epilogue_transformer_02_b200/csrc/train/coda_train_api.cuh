@@ -13,24 +13,20 @@ namespace {
 constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
 
 // A launch with programmatic stream serialisation (the kernel waits for the
-// previous one itself), as the GEMMs'.  cluster 0: none.
+// previous one itself), as the GEMMs'.
 template <class... KArgs, class... Args>
-coda_status_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+coda_status_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                          Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, KArgs(args)...) == cudaSuccess ? CODA_OK : CODA_ERR_LAUNCH;
 }
 
@@ -118,7 +114,7 @@ coda_status_t launch_norm8(const uint16_t* x, const uint16_t* res, const uint16_
               : threads <= 256 ? add_rmsnorm_kernel<MX, false, 256, 5>
               : threads <= 512 ? add_rmsnorm_kernel<MX, false, 512, 4>
                                : add_rmsnorm_kernel<MX, false, 1024, 2>;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), threads, 0, 0, s,
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), threads, 0, s,
                     reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(res),
                     reinterpret_cast<const __nv_bfloat16*>(gamma), eps, s_y, reinterpret_cast<__nv_bfloat16*>(h_out),
                     q, sf, amax, r_out, M, static_cast<int>(N), static_cast<int>(nrb));
@@ -324,7 +320,7 @@ coda_status_t coda_embed(const int64_t* tokens, const uint16_t* E, float scale, 
   DevInfo* info;
   const coda_status_t st = current_device(&dev, &info);
   if (st != CODA_OK) return st;
-  return launch_pdl(embed_kernel, dim3(static_cast<unsigned>(blocks)), 32 * kEmbWarps, 0, 0,
+  return launch_pdl(embed_kernel, dim3(static_cast<unsigned>(blocks)), 32 * kEmbWarps, 0,
                     static_cast<cudaStream_t>(stream), tokens, reinterpret_cast<const __nv_bfloat16*>(E), scale,
                     reinterpret_cast<const __nv_bfloat16*>(gamma), reinterpret_cast<__nv_bfloat16*>(h_out),
                     reinterpret_cast<__nv_bfloat16*>(hg_out), partial, M, static_cast<int>(D), V,
@@ -397,7 +393,7 @@ coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float sc
   // once beside the sorting one (a second wave of them took 120 us more)
   const size_t take = size_t(64) * kZeroPiece;
   const int64_t zc = std::min<int64_t>(clusters[dev] - 1, static_cast<int64_t>((zero_row * row + take - 1) / take));
-  st = launch_pdl(embed_sort_kernel, dim3(static_cast<unsigned>(kSortCluster * (1 + zc))), kSortThreads, kSortSmem, 0,
+  st = launch_pdl(embed_sort_kernel, dim3(static_cast<unsigned>(kSortCluster * (1 + zc))), kSortThreads, kSortSmem,
                   s, tokens, static_cast<int>(M), V, passes, b0, b1, reinterpret_cast<uint8_t*>(dE), zero_row * row,
                   bitmap, w.words, crossing);
   if (st != CODA_OK) return st;
@@ -405,12 +401,12 @@ coda_status_t coda_embed_bwd(const int64_t* tokens, const uint16_t* dh, float sc
   const int spans = embed_bwd_spans(D), unit = embed_bwd_unit(D);
   const int64_t zb = accumulate ? 0 : (V - zero_row + (1 << unit) - 1) >> unit;
   auto sum = accumulate ? embed_bwd_kernel<true> : embed_bwd_kernel<false>;
-  st = launch_pdl(sum, dim3(static_cast<unsigned>(w.items * spans + zb)), threads, 0, 0, s, pairs,
+  st = launch_pdl(sum, dim3(static_cast<unsigned>(w.items * spans + zb)), threads, 0, s, pairs,
                   reinterpret_cast<const __nv_bfloat16*>(dh), scale, dE, part, list, crossing, static_cast<int>(M), V,
                   static_cast<int>(D), w.chunk, w.items, spans, static_cast<const uint32_t*>(bitmap), zero_row, unit);
   if (st != CODA_OK || w.items == 1) return st;
   const int64_t jb = std::min<int64_t>(2 * info->sms, (w.items - 1) * ((D + 255) / 256));
-  return launch_pdl(embed_bwd_join_kernel, dim3(static_cast<unsigned>(jb)), 32 * kJoinGroups, 0, 0, s, pairs,
+  return launch_pdl(embed_bwd_join_kernel, dim3(static_cast<unsigned>(jb)), 32 * kJoinGroups, 0, s, pairs,
                     static_cast<const float*>(part), static_cast<const int*>(list), static_cast<const int*>(crossing),
                     scale, dE, static_cast<int>(D), w.chunk, w.items, accumulate ? 1 : 0);
 }
@@ -478,12 +474,12 @@ coda_status_t coda_add_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const 
                                   : threads <= 256 ? add_rmsnorm_bwd_kernel<false, 256, 4>
                                   : threads <= 512 ? add_rmsnorm_bwd_kernel<false, 512, 2>
                                                    : add_rmsnorm_bwd_kernel<false, 1024, 1>);
-  st = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), threads, 0, 0, s,
+  st = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), threads, 0, s,
                   reinterpret_cast<const __nv_bfloat16*>(dy), reinterpret_cast<const __nv_bfloat16*>(h), r,
                   reinterpret_cast<const __nv_bfloat16*>(gamma), reinterpret_cast<const __nv_bfloat16*>(d_h),
                   reinterpret_cast<__nv_bfloat16*>(dx_out), static_cast<float*>(ws), M, static_cast<int>(N));
   if (st != CODA_OK) return st;
-  return launch_pdl(norm8_dgamma_kernel, dim3(static_cast<unsigned>((N + 31) / 32)), 1024, 0, 0, s,
+  return launch_pdl(norm8_dgamma_kernel, dim3(static_cast<unsigned>((N + 31) / 32)), 1024, 0, s,
                     static_cast<const float*>(ws), blocks, static_cast<int>(N), dgamma_out);
 }
 
@@ -532,10 +528,10 @@ coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, i
   if (!ok) return CODA_ERR_INTERNAL;
   const size_t n8 = static_cast<size_t>(m) * n / 8;
   st = launch_pdl(ns_sumsq_kernel, dim3(static_cast<unsigned>(pl.norm_blocks), static_cast<unsigned>(batch)),
-                  kNsNormThreads, 0, 0, stm, G, n8, pl.norm_blocks, sums);
+                  kNsNormThreads, 0, stm, G, n8, pl.norm_blocks, sums);
   if (st != CODA_OK) return st;
   st = launch_pdl(ns_scale_kernel, dim3(static_cast<unsigned>(pl.norm_blocks), static_cast<unsigned>(batch)),
-                  kNsNormThreads, 0, 0, stm, G, n8, pl.norm_blocks, static_cast<const double*>(sums),
+                  kNsNormThreads, 0, stm, G, n8, pl.norm_blocks, static_cast<const double*>(sums),
                   static_cast<double>(eps), hi[0], lo[0], p.counters,
                   ns_counters(batch));
   if (st != CODA_OK) return st;
