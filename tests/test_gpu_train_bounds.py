@@ -90,6 +90,102 @@ def test_newton_schulz_of_a_gradient_with_feature_means(m, n, means):
     assert e <= math.sqrt(stated(m, n) ** 2 + slack), e
 
 
+# The kernel's roundings restated: fp16 values scaled by powers of two, the
+# symmetric results' lower halves mirrored, what fp16 drops of a diagonal kept
+# beside it, X in two parts of which the last update takes the first.
+
+
+def f16(x, scale):
+    return (x * scale).to(torch.float16).to(F64) / scale
+
+
+class Sym:
+    def __init__(self, v, scale, diag):
+        v = torch.tril(v) + torch.tril(v, -1).t()
+        self.m = f16(v, scale)
+        self.f = torch.diagonal(self.m)
+        self.d = (torch.diagonal(v) - self.f) * (1.0 if diag else 0.0)
+
+
+def truncated_product(x, y):
+    """Sums of 16 products at a time, each addition cut to fp32's 24 bits."""
+    acc = torch.zeros(x.shape[0], y.shape[1], dtype=F64, device="cuda")
+    for k in range(0, x.shape[1], 16):
+        mant, ex = torch.frexp(acc + x[:, k:k + 16] @ y[k:k + 16])
+        acc = torch.ldexp(torch.trunc(mant * 2.0 ** 24) / 2.0 ** 24, ex)
+    return acc
+
+
+def ns_restated(G, product=torch.matmul, diag=True, low=True):
+    a, b, c = C.NEWTON_SCHULZ_COEFFS
+    X = G.to(F64)
+    X = X / (X.norm() + 1e-7)
+    X = X.t() if X.shape[0] > X.shape[1] else X
+    for step in range(5):
+        hi = f16(X, 4096.0)
+        lo = f16(X - hi, 4096.0) * (1.0 if low and step < 4 else 0.0)
+        A = Sym(product(hi, hi.t()), 1024.0, diag)
+        corr = c * (2 * A.d * A.f + A.d * A.d) + b * A.d + a
+        P = Sym(c * product(A.m, A.m) + b * A.m + torch.diag(corr), 256.0, diag)
+        X = product(P.m, hi) + P.d[:, None] * hi + (P.d + P.f)[:, None] * lo
+    return X.t() if G.shape[0] > G.shape[1] else X
+
+
+def ns_case(kind, m, n):
+    g = gen(m + 3 * n)
+    if kind == "gaussian":
+        return randn(g, m, n)
+    if kind == "one direction":
+        return low_rank(g, m, n, 1, 1e-3)
+    if kind == "means":
+        T = 2 * min(m, n)
+        return (randn(g, m, T) + 3 * randn(g, m, 1)) @ (randn(g, T, n) + 3 * randn(g, 1, n))
+    q, r = torch.linalg.qr(randn(g, max(m, n), min(m, n)))  # every A and P a multiple of the identity
+    return (q if m > n else q.t()).contiguous()
+
+
+@pytest.mark.parametrize("kind,m,n", [(k, m, n) for k in ("gaussian", "one direction", "means")
+                                      for m, n in ((512, 512), (384, 1160), (1160, 384), (1024, 1032))]
+                         + [("orthogonal", 512, 512), ("orthogonal", 384, 1160)])
+def test_newton_schulz_rounds_as_stated(kind, m, n):
+    """The result is that of the stated roundings with exact sums, up to what the
+    tensor core's fp32 sums move: an entry whose sum is cut differently may round
+    to the fp16 value beside it.  How far that reaches is worked out with sums cut
+    after every 16 products (3e-4 to 1.1e-3 for these inputs); the bar is a third
+    above it.  Without the diagonals' corrections the result would be 1.0e-3 to
+    2.3e-3 away, without X's low part up to 0.12: both beyond the bar."""
+    G = ns_case(kind, m, n)
+    ref = ns_restated(G)
+
+    def away(X):
+        return float((X - ref).norm() / ref.norm())
+
+    bar = 4 / 3 * away(ns_restated(G, truncated_product)) + 5e-5
+    assert bar < away(ns_restated(G, diag=False))
+    if kind != "gaussian":
+        assert bar < away(ns_restated(G, low=False))
+    e, slack = ns_error(C.newton_schulz(G), ref)
+    assert e <= math.sqrt(bar ** 2 + slack), (e, bar)
+
+
+@pytest.mark.parametrize("batch,m,n", [(9, 264, 256), (3, 520, 512), (40, 72, 136), (2, 1032, 520)])
+def test_newton_schulz_matrix_of_a_batch_is_what_it_is_alone(batch, m, n):
+    """To the last bit where the sums' k-blocks stay whole (K below 1024).  A K of
+    1032 has 17 k-blocks, which the batch's 128 x 128 tiles take in two parts and
+    the 128 x 64 ones of a matrix alone in one: another order of sums, so there
+    each is within the stated bound of the exact X and within half a bf16 step of
+    its own, and the two differ by no more than twice both."""
+    G = randn(gen(batch + m), batch, m, n)
+    out = C.newton_schulz(G)
+    for i in range(batch):
+        alone = C.newton_schulz(G[i])
+        if max(m, n) < 1024:
+            assert torch.equal(alone, out[i])
+        else:
+            far = (alone.to(F64) - out[i].to(F64)).norm() / out[i].to(F64).norm()
+            assert float(far) <= 2 * (stated(m, n) + 2.0 ** -8)
+
+
 # --------------------------------------------------------------- 8-bit norm
 
 
