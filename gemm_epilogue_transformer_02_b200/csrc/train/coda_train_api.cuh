@@ -139,9 +139,15 @@ constexpr int kNsFew = 4;
 
 inline int ns_counters(int64_t batch) { return static_cast<int>(batch) + kNsKinds * kNsSplitCounters; }
 
+// The longest side, which a Gram matrix sums over: its one tile of a narrow matrix,
+// in two parts, takes 0.25 us for each of their 64-wide k-blocks (0.65 s for five
+// steps at 8 x 2^26), and the other CTAs' waits for a part end after a second.
+constexpr int64_t kNsMaxSide = int64_t(1) << 28;
+
 // (byte strides of the tensor maps; tiles are counted in ints)
 inline bool ns_shape_ok(int64_t batch, int64_t m, int64_t n) {
-  return batch >= 0 && batch <= 65535 && dim_ok(m) && dim_ok(n) && m * n <= int64_t(1) << 38 &&
+  return batch >= 0 && batch <= 65535 && dim_ok(m) && dim_ok(n) && std::max(m, n) <= kNsMaxSide &&
+         m * n <= int64_t(1) << 38 &&
          2 * batch * ((m + 127) / 128) * ((n + 63) / 64) <= kMaxInt;
 }
 

@@ -570,7 +570,8 @@ size_t coda_newton_schulz_workspace_size(int64_t batch, int64_t m, int64_t n);
  * 256 (a I + b A + c A^2) become infinite.  A matrix with a non-finite entry
  * gives a non-finite result and leaves the others of the batch alone; a zero
  * matrix gives zeros if eps > 0.
- * m and n multiples of 8, m * n <= 2^38, 1 <= steps <= 100, batch <= 65535. */
+ * m and n multiples of 8, at most 2^28, m * n <= 2^38, 1 <= steps <= 100, batch
+ * <= 65535. */
 coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, int64_t m, int64_t n, int steps, float a,
                                  float b, float c, float eps, void* ws, size_t ws_bytes, void* stream);
 

@@ -30,3 +30,13 @@ def test_embed_grid(lib):
 def test_embed_bwd_grid(lib, M, D, V, accumulate):
     assert lib.coda_embed_bwd(P, Q, 1.0, R, accumulate, S, (1 << 63) - 1, M, D, V, None) == SHAPE
     assert lib.coda_embed_bwd_workspace_size(M, D, V) == 0
+
+
+def test_newton_schulz_longest_side(lib):
+    """A sum over 2^29 takes longer than the waits for it last (0.25 us for 64 of them)."""
+    f, size, c = lib.coda_newton_schulz, lib.coda_newton_schulz_workspace_size, (3.4445, -4.775, 2.0315)
+    long = 1 << 28
+    assert size(1, 8, long) > 0 and size(1, long, 8) > 0
+    for m, n in ((8, long + 8), (long + 8, 8), (8, 1 << 29), (1 << 29, 16)):
+        assert size(1, m, n) == 0
+        assert f(P, Q, 1, m, n, 5, *c, 1e-7, R, (1 << 63) - 1, None) == SHAPE
