@@ -7,9 +7,9 @@
 //             dgamma = sum_i dy (r h)
 //
 // Each element is read once and each output written once; both are bound by
-// HBM (7 and 8 bytes an element).  A row lives in the registers of one block
-// or warp from its load to its store: sums, r and y are fp32, h and dx are rounded to
-// bf16 once.
+// HBM (7 and 8 bytes an element).  A row lives in the registers of one block or
+// warp from its load to its store: sums, r and y are fp32, h and dx are rounded
+// to bf16 once.
 #pragma once
 
 #include "coda_embed.cuh"
@@ -151,11 +151,12 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_kernel(
 // by norm8_dgamma_kernel in a fixed order.  What bounds it is how much is in
 // flight.  Up to 128 threads (2048 columns) the next row's vectors are requested
 // before this row's sum is reduced, in as many blocks (BLOCKS of MAXT threads on
-// an SM) as have registers for both rows: 8192 x 2048 with 4 blocks 28.8 us, 5
-// 24.7, 6 32.4, without the next row and 8 blocks 27.5; bulk copies into a ring
-// of shared memory 45, two rows ahead 29.3.  Wider rows are better off with twice
-// the blocks and one row each (with norm8_dgamma_kernel, 8192 x 4096: 50.3 us
-// against 59.0, 4096 x 4104 32.0 against 50.5, 4096 x 8192 51.1 against 66.3).
+// an SM) as have registers for both rows: 8192 x 2048 with 4 or 5 blocks 24.7 us,
+// 6 31.9, without the next row and 8 blocks 28.1; 8192 x 1536 with 4 21.3, with 5
+// 20.4.  Wider rows are better off with twice the blocks and one row each (8192 x
+// 4096: 50.3 us against 59.0, 4096 x 4104 32.0 against 50.5, 4096 x 8192 51.1
+// against 66.3).  Times are of the whole call, this launch and
+// norm8_dgamma_kernel, back to back with its outputs given.
 template <bool WARP, int MAXT, int BLOCKS>
 __global__ void __launch_bounds__(MAXT, BLOCKS) add_rmsnorm_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ h, const float* __restrict__ r,

@@ -213,11 +213,6 @@ __device__ __forceinline__ uint64_t f2_half(uint32_t h) {  // two fp16 values
   const float2 f = unpack_f16x2(h);
   return f2_set(f.x, f.y);
 }
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -662,15 +657,19 @@ __device__ __forceinline__ bool ns_epilogue(const NsParams& p, int step, const N
 // the epilogue warps go on through an mbarrier.  One counter for all matrices
 // makes that a barrier between GEMMs, and the CTAs arrive once for a phase.  With
 // a few units for each CTA (`few`) each matrix has its own, and the last units of
-// one phase run beside the first of the next: 575 against 626 us for four of 2048
-// x 2048, 239 against 264 for eight of 1024 x 1024, 128 against 154 for sixteen of
-// 512 x 512 (but 90.8 against 88.9 for four of them, one unit for each CTA).  With
-// many units the phases' ends matter less than an arrival for each unit: 64 of
-// 512 x 512 took 415 against 390.  Every buffer is written one phase or more
-// after the phases that read it, of the same matrix.  The split tiles' exchange
-// buffers are no matrix's: their units wait for all matrices.  A unit only waits
-// for units before it in the order that all CTAs follow, and all CTAs are
-// resident at once, by a cooperative launch.
+// one phase run beside the first of the next: 586 against 626 us for four of 2048
+// x 2048, 237 against 270 for eight of 1024 x 1024, 125 against 153 for sixteen of
+// 512 x 512.  With many units the phases' ends matter less than an arrival for
+// each: 706 against 674 for 128 of 512 x 512, 990 against 735 for 3000 of 64 x 64
+// (equal within 5 % at seven units for each CTA).  Every buffer is written one
+// phase or more after the phases that read it, of the same matrix.  The split
+// tiles' exchange buffers are no matrix's: their units wait for all matrices.  A
+// unit only waits for units before it in the order that all CTAs follow, and all
+// CTAs are resident at once, by a cooperative launch.
+//
+// Times here and at the tile rule: calls back to back with normal entries in G.
+// Where a gradient's products keep the clock lower they are longer (690 us for
+// four of 2048 x 2048).
 template <class T>
 __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant__ NsParams p) {
   constexpr bool PAIR = T::kPair;
