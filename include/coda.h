@@ -563,13 +563,13 @@ size_t coda_newton_schulz_workspace_size(int64_t batch, int64_t m, int64_t n);
  * and out = bf16(X).  G [batch, m, n] fp32 (a gradient or momentum, such as the
  * backward calls give), out [batch, m, n] bf16.  The products take fp16
  * operands with fp32 sums and corrections for their rounding: after five steps
- * about 1e-3 of |X|_F from exact arithmetic before the output's rounding (itself
- * 1.7e-3), and where one or a few directions hold G's norm up to 1.5e-3 + 0.65 /
- * min(m, n).  The coefficients must keep the singular values bounded, as Muon's
- * (3.4445, -4.775, 2.0315) do: intermediate values beyond 16 (X), 64 (A) or
- * 256 (a I + b A + c A^2) become infinite.  A matrix with a non-finite entry
- * gives a non-finite result and leaves the others of the batch alone; a zero
- * matrix gives zeros if eps > 0.
+ * the result is up to 1.5e-3 + 0.65 / min(m, n) of |X|_F from exact arithmetic
+ * before the output's rounding (itself 1.7e-3); about 1e-3 from a side of 64 on
+ * if more than a few directions hold G's norm.  The coefficients must keep the
+ * singular values bounded, as Muon's (3.4445, -4.775, 2.0315) do: intermediate
+ * values beyond 16 (X), 64 (A) or 256 (a I + b A + c A^2) become infinite.  A
+ * matrix with a non-finite entry gives a non-finite result and leaves the others
+ * of the batch alone; a zero matrix gives zeros if eps > 0.
  * m and n multiples of 8, at most 2^28, m * n <= 2^38, 1 <= steps <= 100, batch
  * <= 65535. */
 coda_status_t coda_newton_schulz(const float* G, uint16_t* out, int64_t batch, int64_t m, int64_t n, int steps, float a,
