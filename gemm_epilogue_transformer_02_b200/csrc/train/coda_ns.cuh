@@ -44,7 +44,7 @@
 // correlated matrices after five steps (sides of 64 and more).  Where a few
 // directions hold the norm the others lie in the low part, which sees only P's
 // diagonal, and the entries of P beside it, of 2.7 / s for one direction, are
-// what is left out: with the smaller side s up to 1e-3 + 0.65 / s.  Plain bf16
+// what is left out: with the smaller side s up to 1.5e-3 + 0.65 / s.  Plain bf16
 // products give 0.9e-2 and 3e-1.  The bf16 rounding of the output alone is
 // 1.7e-3.
 #pragma once
